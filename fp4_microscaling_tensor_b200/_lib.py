@@ -29,7 +29,8 @@ EXPORTS = ("mx_quantize", "mx_dequantize", "mx_error_stats_workspace_size", "mx_
            "mx_global_scale_group", "mx_error_stats_means",
            "mx_fake_quantize", "mx_matmul_scales_size", "mx_matmul_prepare_scales",
            "mx_matmul", "mx_matmul_pair", "mx_dequant_matmul", "mx_matmul_gave_up",
-           "mx_test_matmul_abandon_last",
+           "mx_test_matmul_abandon_last", "mx_cache_append", "mx_cache_read",
+           "mx_cache_attention", "mx_cache_attention_workspace_size",
            "mx_test_fail_next_calls", "mx_status_string", "mx_kernel_launches")
 MX_MAX_GROUP = 16
 
@@ -44,6 +45,19 @@ class Tensor(ctypes.Structure):
 
 
 assert ctypes.sizeof(Tensor) == 72
+
+
+class Cache(ctypes.Structure):
+    """mx_cache_t: a paged FP4 key/value cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("fmt", ctypes.c_int32),
+                ("k_global_scale_fp16", ctypes.c_uint16), ("v_global_scale_fp16", ctypes.c_uint16)]
+
+
+assert ctypes.sizeof(Cache) == 64
 
 _i, _i64, _u16, _vp, _sz = ctypes.c_int, ctypes.c_int64, ctypes.c_uint16, ctypes.c_void_p, ctypes.c_size_t
 
@@ -92,6 +106,19 @@ lib.mx_matmul_prepare_scales.restype = _i
 lib.mx_matmul_prepare_scales.argtypes = [_vp, _i64, _i64, _vp, _sz, _vp]
 lib.mx_matmul_gave_up.restype = _i
 lib.mx_matmul_gave_up.argtypes = [ctypes.POINTER(ctypes.c_uint)]
+Strides = _i64 * 3
+_cp, _st = ctypes.POINTER(Cache), ctypes.POINTER(_i64)
+lib.mx_cache_append.restype = _i
+lib.mx_cache_append.argtypes = [_cp, _vp, _vp, _i, _st, _st, _i64, _i64, _vp, _i64, _i64, _vp, _vp,
+                                _vp]
+lib.mx_cache_read.restype = _i
+lib.mx_cache_read.argtypes = [_cp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i, _st, _st,
+                              _vp]
+lib.mx_cache_attention_workspace_size.restype = _sz
+lib.mx_cache_attention_workspace_size.argtypes = [_i64] * 5
+lib.mx_cache_attention.restype = _i
+lib.mx_cache_attention.argtypes = [_cp, _vp, _st, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp,
+                                   ctypes.c_float, _vp, _st, _vp, _vp, _sz, _vp]
 lib.mx_status_string.restype = ctypes.c_char_p
 lib.mx_status_string.argtypes = [_i]
 lib.mx_kernel_launches.restype = ctypes.c_longlong

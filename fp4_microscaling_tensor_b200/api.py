@@ -1,9 +1,11 @@
-"""Python API over the C ABI: quantize, dequantize, error_stats, global_scale, matmul.
+"""Python API over the C ABI: quantize, dequantize, error_stats, global_scale, matmul, and a paged
+FP4 key/value cache (KVCache, cache_append, cache_read, cache_attention).
 
 Tensors are CUDA tensors, contiguous, row-major, with blocks along the last dimension.  Outputs are
 allocated with torch on the tensor's device unless given.  Calls are asynchronous on the current
 torch stream (or `stream=`); nothing here synchronizes except ErrorStats.to_dict().
 """
+import contextlib
 import ctypes
 import struct
 
@@ -11,7 +13,7 @@ import numpy as np
 import torch
 
 from ._lib import (MX_BF16, MX_F32, MX_MAX_GROUP, MX_SCALE_E4M3, MX_SCALE_UE5M3,  # noqa: F401
-                   MXError, Tensor, check, lib)
+                   Cache, MXError, Strides, Tensor, check, lib)
 
 E4M3, UE5M3 = MX_SCALE_E4M3, MX_SCALE_UE5M3
 _FMT = {"e4m3": E4M3, "ue5m3": UE5M3, E4M3: E4M3, UE5M3: UE5M3}
@@ -451,6 +453,207 @@ def dequant_matmul(a, w_packed, w_scales, block=32, fmt="ue5m3", g=None, out_dty
                                 int(block), fmt_code(fmt), gb, g_dev, out.data_ptr(),
                                 _DT[out.dtype], _stream(stream, a.device)), "mx_dequant_matmul")
     return out
+
+
+# ---- a paged FP4 key/value cache -----------------------------------------------------------------
+
+class KVCache:
+    """FP4 key/value cache of one layer: `pages` pages of `page_size` slots, a slot holding one
+    token's keys and values of every head, quantized in blocks of `block` along the head.
+
+    k_codes, v_codes    uint8 [pages, kv_heads, page_size, head_dim / 2], packed as quantize() does
+    k_scales, v_scales  uint8 [pages, kv_heads, page_size, head_dim / block]
+    k_g, v_g            FP16 factors of the keys and the values (a value or a bit pattern; fixed
+                        for the cache's life, so take them from calibration, e.g. global_scale())
+
+    Which pages belong to which sequence is the caller's: position p of sequence b is slot
+    p % page_size of page table[b, p // page_size] of the int32 table given to each call."""
+
+    def __init__(self, pages, kv_heads, head_dim, page_size=64, block=32, fmt="e4m3", k_g=None,
+                 v_g=None, device="cuda"):
+        if min(pages, kv_heads, page_size) < 1 or head_dim not in (64, 128, 256) or \
+                block not in (16, 32, 64, 128) or block > head_dim:
+            raise ValueError("KVCache: head_dim 64, 128 or 256; block 16, 32, 64 or 128 and at "
+                             "most head_dim; pages, kv_heads and page_size positive")
+        lead = (pages, kv_heads, page_size)
+        self._set(*(torch.zeros(lead + (n,), dtype=torch.uint8, device=device)
+                    for n in (head_dim // 2, head_dim // block) * 2), fmt, k_g, v_g)
+
+    @classmethod
+    def from_buffers(cls, k_codes, k_scales, v_codes, v_scales, fmt="e4m3", k_g=None, v_g=None):
+        """A cache over memory that the caller holds (the four tensors above)."""
+        self = cls.__new__(cls)
+        self._set(k_codes, k_scales, v_codes, v_scales, fmt, k_g, v_g)
+        return self
+
+    def _set(self, k_codes, k_scales, v_codes, v_scales, fmt, k_g, v_g):
+        for t in (k_codes, k_scales, v_codes, v_scales):
+            if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != 4 or not t.is_contiguous() or \
+                    t.device != k_codes.device:
+                raise ValueError("KVCache: contiguous 4-D uint8 CUDA tensors on one device")
+        if k_codes.shape != v_codes.shape or k_scales.shape != v_scales.shape or \
+                k_codes.shape[:3] != k_scales.shape[:3]:
+            raise ValueError("KVCache: codes [pages, kv_heads, page_size, head_dim / 2] and scales "
+                             "[pages, kv_heads, page_size, head_dim / block] of keys and values")
+        self.pages, self.kv_heads, self.page_size, half = k_codes.shape
+        self.head_dim = 2 * half
+        if not k_scales.shape[3] or self.head_dim % k_scales.shape[3]:
+            raise ValueError("KVCache: head_dim / block scales per head")
+        self.block = self.head_dim // k_scales.shape[3]
+        if self.head_dim not in (64, 128, 256) or self.block not in (16, 32, 64, 128) or \
+                self.page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("KVCache: head_dim 64, 128 or 256, block 16, 32, 64 or 128, page_size "
+                             "16, 32, 64, 128 or 256")
+        self.fmt, self.device = fmt_code(fmt), k_codes.device
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_g, self.v_g = g_bits(k_g), g_bits(v_g)
+        self._desc = Cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                           v_scales.data_ptr(), self.pages, self.kv_heads, self.page_size,
+                           self.head_dim, self.block, self.fmt, self.k_g, self.v_g)
+
+
+def _strides(t):
+    """The first three strides of a [batch, tokens, heads, head_dim] tensor (0 where the dimension
+    has one entry: it is never stepped over)."""
+    return Strides(*(st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape[:3])))
+
+
+def _outside(t, what, cache, dtypes, shape=None, written=False):
+    """Checks a [batch, tokens, heads, head_dim] tensor given to a cache call."""
+    if t.dim() != 4 or t.device != cache.device or t.dtype not in dtypes:
+        raise ValueError(f"{what}: a 4-D tensor [batch, tokens, heads, head_dim] on the cache's "
+                         f"device, {' or '.join(str(d).split('.')[1] for d in dtypes)}")
+    if t.shape[3] != cache.head_dim or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} does not fit")
+    if t.stride(3) != 1 or (written and any(n > 1 and st == 0
+                                            for n, st in zip(t.shape, t.stride()))):
+        raise ValueError(f"{what}: the last dimension contiguous"
+                         + (", no dimension expanded" if written else ""))
+
+
+def _sequences(cache, batch, table, first, count, what):
+    """Checks the page table and the per-sequence numbers; their addresses and the table's shape."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.device != cache.device or \
+            table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table: int32 [batch, max_pages] on the cache's device, rows contiguous")
+    for t, name in ((first, what), (count, "count")):
+        if t is None and name == "count":
+            continue
+        if t.dtype != torch.int32 or t.shape != (batch,) or t.device != cache.device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous int32 [batch] on the cache's device")
+    return (table.data_ptr(), table.stride(0) if batch > 1 else 0, table.shape[1],
+            first.data_ptr(), None if count is None else count.data_ptr())
+
+
+def _allocating(stream):
+    """Where outputs and scratch are allocated (and zeroed): on the stream that uses them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream)))
+
+
+def _call(fn, where, device, *args):
+    """fn(*args) with the device current that the tensors live on."""
+    if device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    check(status, where)
+
+
+def _new(shape, dtype, cache, count, stream):
+    """A new output; zeros where a count may leave rows of it unwritten."""
+    with _allocating(stream):
+        make = torch.empty if count is None else torch.zeros
+        return make(shape, dtype=dtype, device=cache.device)
+
+
+def cache_append(cache, k, v, table, start, count=None, stream=None):
+    """Quantizes keys and values into the cache: token t < count[b] of k, v [batch, tokens,
+    kv_heads, head_dim] (bf16 or fp32, any strides that are multiples of 16 bytes, e.g. slices of a
+    fused projection) becomes position start[b] + t of sequence b; codes and scales are those of
+    quantize().  table int32 [batch, max_pages], start and count int32 [batch], on the device.
+    Tokens behind count (padding) are not read; positions without a page are not written."""
+    _outside(k, "k", cache, (torch.bfloat16, torch.float32))
+    _outside(v, "v", cache, (k.dtype,), k.shape)
+    if k.shape[2] != cache.kv_heads:
+        raise ValueError(f"k: {cache.kv_heads} heads in the cache")
+    batch, tokens = k.shape[:2]
+    at = _sequences(cache, batch, table, start, count, "start")
+    _call(lib.mx_cache_append, "mx_cache_append", cache.device, cache._desc, k.data_ptr(),
+          v.data_ptr(), _DT[k.dtype], _strides(k), _strides(v), batch, tokens, *at,
+          _stream(stream, cache.device))
+
+
+def cache_read(cache, table, start, count, tokens, out_dtype=torch.bfloat16, k_out=None, v_out=None,
+               stream=None):
+    """Reads keys and values back: (k, v) [batch, tokens, kv_heads, head_dim] whose token
+    t < count[b] is position start[b] + t, the values of dequantize() (count None: all tokens).
+    Rows behind count keep what k_out / v_out hold, or are zero in new tensors; positions without a
+    page read as zeros."""
+    batch, shape = table.shape[0], (table.shape[0], int(tokens), cache.kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = _new(shape, out_dtype if v_out is None else v_out.dtype, cache, count, stream)
+    if v_out is None:
+        v_out = _new(shape, k_out.dtype, cache, count, stream)
+    _outside(k_out, "k_out", cache, (torch.bfloat16, torch.float32), shape, written=True)
+    _outside(v_out, "v_out", cache, (k_out.dtype,), shape, written=True)
+    at = _sequences(cache, batch, table, start, count, "start")
+    _call(lib.mx_cache_read, "mx_cache_read", cache.device, cache._desc, *at, batch, int(tokens),
+          k_out.data_ptr(), v_out.data_ptr(), _DT[k_out.dtype], _strides(k_out), _strides(v_out),
+          _stream(stream, cache.device))
+    return k_out, v_out
+
+
+def attention_workspace(cache, batch, tokens, heads, device=None):
+    """Scratch for cache_attention() calls of this shape that do not run at the same time."""
+    n = lib.mx_cache_attention_workspace_size(batch, tokens, heads, cache.kv_heads, cache.head_dim)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device if device is None else device)
+
+
+def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Attention of the newest tokens of each sequence over the cache: q [batch, tokens, heads,
+    head_dim] bf16 (heads a multiple of the cache's; strided as in cache_append); sequence b is
+    length[b] positions long, the last count[b] (default: tokens) of which are those of this call,
+    already appended.  A token sees every earlier position and, of this call's tokens, itself and
+    those before it, or with tree (int64 [batch, tokens], tokens <= 64) token j where bit j of its
+    word is set: the ancestors, and usually itself, in a tree of drafted tokens.  Tokens that see
+    nothing get zeros.  After a draft is verified, append the accepted tokens' keys and values again
+    behind each other.
+
+    scale defaults to head_dim ** -0.5.  Returns out (bf16, like q), or (out, lse) when lse is True
+    or a float32 [batch, tokens, heads] tensor: the log of the sum of exponentials, -inf for a
+    token that sees nothing.  Rows behind count keep what out and lse hold, or are zero in new
+    tensors."""
+    _outside(q, "q", cache, (torch.bfloat16,))
+    batch, tokens, heads, dim = q.shape
+    if heads < 1 or heads % cache.kv_heads:
+        raise ValueError(f"q: a multiple of the cache's {cache.kv_heads} heads")
+    at = _sequences(cache, batch, table, length, count, "length")
+    if tree is not None and (tree.dtype != torch.int64 or tuple(tree.shape) != (batch, tokens)
+                             or tree.device != cache.device or not tree.is_contiguous()):
+        raise ValueError("tree: contiguous int64 [batch, tokens] on the cache's device")
+    if out is None:
+        out = _new(q.shape, torch.bfloat16, cache, count, stream)
+    _outside(out, "out", cache, (torch.bfloat16,), q.shape, written=True)
+    if lse is True:
+        lse = _new((batch, tokens, heads), torch.float32, cache, count, stream)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (batch, tokens, heads)
+                            or lse.device != cache.device or not lse.is_contiguous()):
+        raise ValueError("lse: contiguous float32 [batch, tokens, heads] on the cache's device")
+    if workspace is None:
+        with _allocating(stream):
+            workspace = attention_workspace(cache, batch, tokens, heads)
+    _call(lib.mx_cache_attention, "mx_cache_attention", cache.device, cache._desc, q.data_ptr(),
+          _strides(q), batch, tokens, heads, *at, None if tree is None else tree.data_ptr(),
+          float(dim ** -0.5 if scale is None else scale), out.data_ptr(), _strides(out),
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+          _stream(stream, cache.device))
+    return out if lse is None else (out, lse)
 
 
 def matmul_gave_up():

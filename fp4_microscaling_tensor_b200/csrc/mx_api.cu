@@ -1,15 +1,16 @@
 // mx_api.cu -- the C ABI declared in include/mx.h: argument checks on the host, then the kernel
-// launches of mx_quantize.cu, mx_dequantize.cu, mx_error_stats.cu and mx_global_scale.cu on the
-// caller's stream.  Nothing is allocated and nothing is synchronized here.
+// launches of the other .cu files on the caller's stream.  Nothing is allocated and nothing is synchronized here.
 #include <atomic>
 #include <cmath>
 
 #include "../../include/mx.h"
+#include "mx_cache.h"
 #include "mx_device.cuh"
 #include "mx_launch.h"
 
 static_assert(sizeof(mx_error_stats_t) == 64, "mx_error_stats_t layout");
 static_assert(sizeof(mx_tensor_t) == 72, "mx_tensor_t layout");
+static_assert(sizeof(mx_cache_t) == 64, "mx_cache_t layout");
 static_assert(MX_MAX_GROUP == mxk::kMaxGroup, "group size");
 
 namespace {
@@ -53,6 +54,55 @@ mx_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MX_OK : MX_ERR_CU
 
 size_t stats_ws_bytes() { return (size_t)mxk::kMaxReduceCtas * 64; }
 size_t amax_ws_bytes() { return (size_t)mxk::kMaxReduceCtas * 4; }
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+bool valid_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
+
+// Checks a cache descriptor and turns it into kernel parameters.
+mx_status check_cache(const mx_cache_t* c, mxk::CacheArgs* out) {
+  if (!c || !valid_fmt(c->fmt) || !valid_g(c->k_global_scale_fp16) ||
+      !valid_g(c->v_global_scale_fp16) || c->pages < 1 || c->pages >= (int64_t(1) << 31) ||
+      c->kv_heads < 1 || c->kv_heads > 1024)
+    return MX_ERR_INVALID_ARG;
+  if (!valid_head_dim(c->head_dim) || c->block < 16 || c->block > 128 || !valid_block(c->block) ||
+      c->block > c->head_dim || c->page_size < 16 || c->page_size > 256 ||
+      (c->page_size & (c->page_size - 1)) != 0)
+    return MX_ERR_UNSUPPORTED;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return MX_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
+      !aligned16(c->v_scales))
+    return MX_ERR_MISALIGNED;
+  int shift = 4;
+  while ((1 << shift) < c->page_size) ++shift;
+  *out = {{c->k_codes, c->v_codes}, {c->k_scales, c->v_scales}, c->pages, c->kv_heads, c->head_dim,
+          c->block, c->fmt, shift, {c->k_global_scale_fp16, c->v_global_scale_fp16}};
+  return MX_OK;
+}
+
+// Checks the batch and its page table.
+mx_status check_batch(int64_t batch, int64_t tokens, const int32_t* table, int64_t table_stride,
+                      int64_t max_pages, const int32_t* first, const int32_t* count) {
+  if (batch < 0 || tokens < 0 || batch >= (int64_t(1) << 31) || tokens >= (int64_t(1) << 31) ||
+      max_pages < 0 || max_pages >= (int64_t(1) << 31) || table_stride < 0)
+    return MX_ERR_INVALID_ARG;
+  if (batch == 0 || tokens == 0) return MX_OK;
+  if ((max_pages > 0 && !table) || !first) return MX_ERR_INVALID_ARG;
+  if (!aligned(table, 4) || !aligned(first, 4) || !aligned(count, 4)) return MX_ERR_MISALIGNED;
+  return MX_OK;
+}
+
+// An outside tensor: its address and its three strides (elements of `size` bytes).
+mx_status check_rows(const void* p, const int64_t* strides, int size, mxk::Rows* out) {
+  if (!p || !strides) return MX_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] < 0) return MX_ERR_INVALID_ARG;
+  if (!aligned16(p)) return MX_ERR_MISALIGNED;
+  for (int i = 0; i < 3; ++i)
+    if ((strides[i] * size) % 16 != 0) return MX_ERR_MISALIGNED;
+  *out = {const_cast<void*>(p), strides[0], strides[1], strides[2]};
+  return MX_OK;
+}
 
 }  // namespace
 
@@ -478,11 +528,106 @@ mx_status mx_global_scale_group(const mx_tensor_t* tensors, int count, mx_dtype 
   return from_cuda(e);
 }
 
+mx_status mx_cache_append(const mx_cache_t* cache, const void* k, const void* v, mx_dtype xt,
+                          const int64_t* k_strides, const int64_t* v_strides, int64_t batch,
+                          int64_t tokens, const int32_t* table, int64_t table_stride,
+                          int64_t max_pages, const int32_t* start, const int32_t* count,
+                          cudaStream_t stream) {
+  mxk::CacheArgs c;
+  if (!valid_dtype(xt)) return MX_ERR_INVALID_ARG;
+  mx_status st = check_cache(cache, &c);
+  if (st == MX_OK)
+    st = check_batch(batch, tokens, table, table_stride, max_pages, start, count);
+  if (st != MX_OK || batch == 0 || tokens == 0) return st;
+  mxk::Rows rk, rv;
+  const int size = xt == MX_BF16 ? 2 : 4;
+  if ((st = check_rows(k, k_strides, size, &rk)) != MX_OK) return st;
+  if ((st = check_rows(v, v_strides, size, &rv)) != MX_OK) return st;
+  if (injected_failure()) return MX_ERR_CUDA;
+  int n = 0;
+  const cudaError_t e =
+      mxk::run_cache_append(c, {table, table_stride, max_pages}, rk, rv, xt == MX_BF16, batch,
+                            tokens, start, count, stream, &n);
+  g_launches += n;
+  return from_cuda(e);
+}
+
+mx_status mx_cache_read(const mx_cache_t* cache, const int32_t* table, int64_t table_stride,
+                        int64_t max_pages, const int32_t* start, const int32_t* count,
+                        int64_t batch, int64_t tokens, void* k, void* v, mx_dtype yt,
+                        const int64_t* k_strides, const int64_t* v_strides, cudaStream_t stream) {
+  mxk::CacheArgs c;
+  if (!valid_dtype(yt)) return MX_ERR_INVALID_ARG;
+  mx_status st = check_cache(cache, &c);
+  if (st == MX_OK)
+    st = check_batch(batch, tokens, table, table_stride, max_pages, start, count);
+  if (st != MX_OK || batch == 0 || tokens == 0) return st;
+  mxk::Rows rk, rv;
+  const int size = yt == MX_BF16 ? 2 : 4;
+  if ((st = check_rows(k, k_strides, size, &rk)) != MX_OK) return st;
+  if ((st = check_rows(v, v_strides, size, &rv)) != MX_OK) return st;
+  if (injected_failure()) return MX_ERR_CUDA;
+  int n = 0;
+  const cudaError_t e =
+      mxk::run_cache_read(c, {table, table_stride, max_pages}, rk, rv, yt == MX_BF16, batch,
+                          tokens, start, count, stream, &n);
+  g_launches += n;
+  return from_cuda(e);
+}
+
+size_t mx_cache_attention_workspace_size(int64_t batch, int64_t tokens, int64_t heads,
+                                         int64_t kv_heads, int64_t head_dim) {
+  if (batch < 0 || tokens < 0 || batch >= (int64_t(1) << 31) || tokens >= (int64_t(1) << 31) ||
+      kv_heads < 1 || kv_heads > 1024 || heads < 1 || heads % kv_heads != 0 ||
+      heads / kv_heads > 64 || !valid_head_dim(head_dim))
+    return 0;
+  return mxk::attention_workspace_bytes(batch, tokens, (int)heads, (int)kv_heads, (int)head_dim);
+}
+
+mx_status mx_cache_attention(const mx_cache_t* cache, const void* q, const int64_t* q_strides,
+                             int64_t batch, int64_t tokens, int64_t heads, const int32_t* table,
+                             int64_t table_stride, int64_t max_pages, const int32_t* length,
+                             const int32_t* count, const uint64_t* tree, float scale, void* out,
+                             const int64_t* out_strides, float* lse, void* workspace,
+                             size_t ws_bytes, cudaStream_t stream) {
+  mxk::AttnArgs a = {};
+  mx_status st = check_cache(cache, &a.c);
+  if (st == MX_OK)
+    st = check_batch(batch, tokens, table, table_stride, max_pages, length, count);
+  if (st != MX_OK) return st;
+  if (heads < 1 || heads % a.c.kv_heads != 0 || !std::isfinite(scale)) return MX_ERR_INVALID_ARG;
+  if (heads / a.c.kv_heads > 64 || (tree && tokens > 64)) return MX_ERR_UNSUPPORTED;
+  if (batch == 0 || tokens == 0) return MX_OK;
+  if ((st = check_rows(q, q_strides, 2, &a.q)) != MX_OK) return st;
+  if ((st = check_rows(out, out_strides, 2, &a.out)) != MX_OK) return st;
+  if (!workspace ||
+      ws_bytes < mx_cache_attention_workspace_size(batch, tokens, heads, a.c.kv_heads,
+                                                   a.c.head_dim))
+    return MX_ERR_WORKSPACE;
+  if (!aligned16(workspace) || !aligned(lse, 4) || !aligned(tree, 8)) return MX_ERR_MISALIGNED;
+  if (injected_failure()) return MX_ERR_CUDA;
+  a.table = {table, table_stride, max_pages};
+  a.batch = batch;
+  a.tokens = tokens;
+  a.heads = (int)heads;
+  a.length = length;
+  a.count = count;
+  a.tree = tree;
+  a.scale = scale;
+  a.lse = lse;
+  a.workspace = workspace;
+  int n = 0;
+  const cudaError_t e = mxk::run_cache_attention(a, stream, &n);
+  g_launches += n;
+  return from_cuda(e);
+}
+
 const char* mx_status_string(mx_status status) {
   switch (status) {
     case MX_OK: return "MX_OK";
     case MX_ERR_INVALID_ARG: return "MX_ERR_INVALID_ARG: invalid argument";
-    case MX_ERR_UNSUPPORTED: return "MX_ERR_UNSUPPORTED: block size not in {4,8,16,32,64,128,256}";
+    case MX_ERR_UNSUPPORTED: return "MX_ERR_UNSUPPORTED: block size not in {4,8,16,32,64,128,256}, or a shape the call "
+                                     "does not offer";
     case MX_ERR_MISALIGNED: return "MX_ERR_MISALIGNED: pointer not 16-byte aligned";
     case MX_ERR_WORKSPACE: return "MX_ERR_WORKSPACE: workspace missing or too small";
     case MX_ERR_CUDA: return "MX_ERR_CUDA: CUDA runtime error while enqueueing";

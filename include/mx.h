@@ -64,7 +64,8 @@ extern "C" {
 typedef enum {
   MX_OK = 0,
   MX_ERR_INVALID_ARG = 1, /* null pointer, negative size, bad enum, bad g */
-  MX_ERR_UNSUPPORTED = 2, /* block not one of 4, 8, 16, 32, 64, 128, 256 */
+  MX_ERR_UNSUPPORTED = 2, /* block not one of 4, 8, 16, 32, 64, 128, 256, or a shape that the call
+                             does not offer (see there) */
   MX_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
   MX_ERR_WORKSPACE = 4,   /* workspace pointer NULL or smaller than the *_workspace_size() value */
   MX_ERR_CUDA = 5         /* the CUDA runtime reported an error while enqueueing */
@@ -317,6 +318,99 @@ MX_API mx_status mx_matmul_gave_up(unsigned int* count);
  * on the current device as abandoned, as a thread block whose waits ran out would.  Later
  * launches must not be affected.  Synchronizes the device. */
 MX_API mx_status mx_test_matmul_abandon_last(void);
+
+/* ---- A paged FP4 key/value cache and attention over it (no counterpart in the pages: the method's
+ * storage, [MX] §1 and §3.1, for what a decoder keeps of the tokens it has seen).
+ *
+ * A cache holds the keys and values of one layer in pages of page_size slots; a slot holds one
+ * token's kv_heads vectors of head_dim values, quantized in blocks of `block` consecutive values of
+ * a head.  Sequences own pages through a table: position p of sequence b is slot p % page_size of
+ * page table[b * table_stride + p / page_size].  The caller hands out the pages; two sequences may
+ * share pages that nobody writes any more.
+ *
+ * Conventions of these calls, beyond those above:
+ *   - Index arrays (table, start, count, length) are int32 in device memory, 4-byte aligned (tree:
+ *     8-byte aligned); they are read when the kernels run, so a captured call follows their
+ *     contents.  count may be NULL: `tokens` for every sequence.  Counts outside [0, tokens] are cut
+ *     to it.
+ *   - Outside tensors are [batch, tokens, heads, head_dim] with strides of their own for the first
+ *     three dimensions, {batch, token, head}, in elements (host array of 3, read during the call);
+ *     the last dimension is contiguous.  Strides are >= 0 and whole multiples of 16 bytes
+ *     (MX_ERR_MISALIGNED); outputs must not overlap themselves.
+ *   - Tokens of a sequence behind its count are neither read nor written: rows of padding keep what
+ *     they hold.
+ *   - A position that the table does not reach (p < 0 or p >= max_pages * page_size), or whose table
+ *     entry names no page of the cache, is not written by mx_cache_append, reads as zeros in
+ *     mx_cache_read and is not attended to.  Entries for positions that no call reaches may hold
+ *     anything.
+ *   - batch == 0 or tokens == 0: nothing is enqueued. */
+typedef struct {
+  uint8_t* k_codes;  /* [pages][kv_heads][page_size][head_dim / 2], E2M1 codes as mx_quantize packs
+                        them */
+  uint8_t* k_scales; /* [pages][kv_heads][page_size][head_dim / block] */
+  uint8_t* v_codes;  /* the same for the values */
+  uint8_t* v_scales;
+  int64_t pages;     /* 1 .. 2^31 - 1 */
+  int32_t kv_heads;  /* 1 .. 1024 */
+  int32_t page_size; /* 16, 32, 64, 128 or 256 slots */
+  int32_t head_dim;  /* 64, 128 or 256 */
+  int32_t block;     /* 16, 32, 64 or 128, at most head_dim */
+  int32_t fmt;       /* mx_scale_fmt */
+  uint16_t k_global_scale_fp16, v_global_scale_fp16; /* g of the keys and of the values */
+} mx_cache_t;
+
+/* Quantizes keys and values into the cache: token t < count[b] of sequence b becomes position
+ * start[b] + t, by the rule of mx_quantize (the same codes and scales, bit for bit).
+ *   k, v   [batch, tokens, kv_heads, head_dim] of type xt.  Values should be finite; an infinity
+ *          stores the largest magnitude, a NaN a finite one (never a NaN scale).
+ * Sequences of one call must not write the same slot. */
+MX_API mx_status mx_cache_append(const mx_cache_t* cache, const void* k, const void* v, mx_dtype xt,
+                                 const int64_t* k_strides, const int64_t* v_strides, int64_t batch,
+                                 int64_t tokens, const int32_t* table, int64_t table_stride,
+                                 int64_t max_pages, const int32_t* start, const int32_t* count,
+                                 cudaStream_t stream);
+
+/* Reads keys and values back: token t < count[b] of the outputs is position start[b] + t, by the
+ * rule of mx_dequantize (MX_F32 exact, MX_BF16 its round-to-nearest-even).
+ *   k, v   OUT [batch, tokens, kv_heads, head_dim] of type yt. */
+MX_API mx_status mx_cache_read(const mx_cache_t* cache, const int32_t* table, int64_t table_stride,
+                               int64_t max_pages, const int32_t* start, const int32_t* count,
+                               int64_t batch, int64_t tokens, void* k, void* v, mx_dtype yt,
+                               const int64_t* k_strides, const int64_t* v_strides,
+                               cudaStream_t stream);
+
+/* Bytes of device workspace mx_cache_attention needs for a shape (0 for an invalid one). */
+MX_API size_t mx_cache_attention_workspace_size(int64_t batch, int64_t tokens, int64_t heads,
+                                                int64_t kv_heads, int64_t head_dim);
+
+/* Attention of each sequence's newest tokens over its cache, those tokens included:
+ *     out[b, t, h] = sum_p softmax_p(scale * q[b, t, h] . K[p, h / (heads / kv_heads)]) V[p, ...]
+ * over the positions p that token t sees, K and V the exact dequantized values.  Sequence b is
+ * length[b] positions long (cut to what the table reaches); its count[b] newest ones are those of
+ * this call's tokens, so token t is position length[b] - count[b] + t and mx_cache_append comes
+ * first.  Token t sees every position before the newest ones, and of those
+ *   tree == NULL   tokens 0 .. t (a chain: one token of a decoder's step, a chunk of a prompt);
+ *   tree != NULL   the tokens j whose bit is set in tree[b * tokens + t] (bit j; itself only if its
+ *                  own bit is set): a tree of drafted tokens.  tokens <= 64 then.
+ * A token that sees nothing gets zeros (and -infinity in lse).
+ *   q      [batch, tokens, heads, head_dim], bf16; heads a multiple of cache->kv_heads, at most
+ *          64 * kv_heads
+ *   scale  finite; usually 1 / sqrt(head_dim)
+ *   out    OUT [batch, tokens, heads, head_dim], bf16
+ *   lse    OUT or NULL: the natural logarithm of the sum of the exponentials, float32,
+ *          [batch, tokens, heads] contiguous
+ *   workspace  device scratch of at least mx_cache_attention_workspace_size() bytes; needs no
+ *          initialisation.  Calls that may run at the same time need one each.
+ * Scores, softmax statistics and sums are kept in float32; the softmax weights enter the product
+ * with V as binary16 relative to the row's largest (2^-11 each).  Results do not depend on the order
+ * in which thread blocks run. */
+MX_API mx_status mx_cache_attention(const mx_cache_t* cache, const void* q,
+                                    const int64_t* q_strides, int64_t batch, int64_t tokens,
+                                    int64_t heads, const int32_t* table, int64_t table_stride,
+                                    int64_t max_pages, const int32_t* length, const int32_t* count,
+                                    const uint64_t* tree, float scale, void* out,
+                                    const int64_t* out_strides, float* lse, void* workspace,
+                                    size_t ws_bytes, cudaStream_t stream);
 
 /* Test hook for error paths (no counterpart in the pages).  The next `count` calls that pass
  * their argument checks and would enqueue work return MX_ERR_CUDA instead, as a failed launch is
