@@ -73,10 +73,11 @@ mx_status check_cache(const mx_cache_t* c, mxk::CacheArgs* out) {
   if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
       !aligned16(c->v_scales))
     return MX_ERR_MISALIGNED;
-  int shift = 4;
+  int shift = 4, log_block = 4;
   while ((1 << shift) < c->page_size) ++shift;
+  while ((1 << log_block) < c->block) ++log_block;
   *out = {{c->k_codes, c->v_codes}, {c->k_scales, c->v_scales}, c->pages, c->kv_heads, c->head_dim,
-          c->block, c->fmt, shift, {c->k_global_scale_fp16, c->v_global_scale_fp16}};
+          c->block, c->fmt, shift, log_block, {c->k_global_scale_fp16, c->v_global_scale_fp16}};
   return MX_OK;
 }
 
@@ -596,7 +597,10 @@ mx_status mx_cache_attention(const mx_cache_t* cache, const void* q, const int64
     st = check_batch(batch, tokens, table, table_stride, max_pages, length, count);
   if (st != MX_OK) return st;
   if (heads < 1 || heads % a.c.kv_heads != 0 || !std::isfinite(scale)) return MX_ERR_INVALID_ARG;
-  if (heads / a.c.kv_heads > 64 || (tree && tokens > 64)) return MX_ERR_UNSUPPORTED;
+  if (heads / a.c.kv_heads > 64 || (tree && tokens > 64) ||
+      tokens * (heads / a.c.kv_heads) >= (int64_t(1) << 31) ||
+      max_pages * cache->page_size > (int64_t(1) << 30))
+    return MX_ERR_UNSUPPORTED;
   if (batch == 0 || tokens == 0) return MX_OK;
   if ((st = check_rows(q, q_strides, 2, &a.q)) != MX_OK) return st;
   if ((st = check_rows(out, out_strides, 2, &a.out)) != MX_OK) return st;

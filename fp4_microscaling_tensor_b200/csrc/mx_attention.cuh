@@ -1,0 +1,240 @@
+// mx_attention.cuh -- what the attention kernels over the FP4 cache share: how the work is cut, the
+// partial results of pieces, and small device helpers.
+//
+// The work of a call is a list of units: the 64-position chunks of every segment, a segment being
+// (sequence, key/value head, tile of query rows).  The query rows of a key/value head are its
+// heads / kv_heads query heads of every token, row r = token r / G, head r % G.  How long the
+// sequences are is known on the device only, so every thread block adds the units up itself and
+// takes an equal share of the list: [W c / n, W (c + 1) / n) for block c of n, whatever the lengths
+// are (with fewer units than blocks the first blocks get one each).  A share covers segments whole, or pieces of at most two (its first and its last one); the
+// pieces of a segment leave their running maximum, sum and unnormalised output in the workspace,
+// and k_attention_join adds them up in the order of the list, so results do not depend on timing.
+#pragma once
+
+#include "mx_cache.h"
+#include "mx_device.cuh"
+
+namespace mxk {
+namespace attn {
+
+constexpr int kUnit = 64;  // positions per unit
+
+// A sequence's numbers, cut to what is there: len positions, of which the newest `count` are this
+// call's tokens, from position base on (negative where the sequence is shorter than its count).
+struct Seq {
+  int len, count, base;
+  __device__ __forceinline__ Seq(const AttnArgs& a, int64_t b) {
+    const int64_t reach = a.table.width << a.c.page_shift;  // at most 2^30
+    len = (int)min((int64_t)max(a.length[b], 0), reach);
+    count = a.count ? (int)min((int64_t)max(a.count[b], 0), a.tokens) : (int)a.tokens;
+    base = len - count;
+  }
+  // Tiles of `rows` query rows, and the positions that the rows of tile rt see at most.
+  __device__ __forceinline__ int tiles(int group, int rows) const {
+    return (int)(((int64_t)count * group + rows - 1) / rows);
+  }
+  __device__ __forceinline__ int end(const AttnArgs& a, int group, int rows, int rt) const {
+    if (a.tree) return len;
+    const int64_t last = ((int64_t)(rt + 1) * rows - 1) / group;  // the tile's last token
+    return max(0, (int)min((int64_t)len, base + min((int64_t)count - 1, last) + 1));
+  }
+};
+
+__device__ __forceinline__ int units_of(int end) { return max(1, (end + kUnit - 1) / kUnit); }
+
+// Units of one key/value head of sequence b.
+__device__ __forceinline__ int64_t head_units(const AttnArgs& a, int64_t b, int group, int rows) {
+  const Seq s(a, b);
+  const int tiles = s.tiles(group, rows);
+  if (a.tree || tiles <= 1) return tiles ? (int64_t)tiles * units_of(s.end(a, group, rows, 0)) : 0;
+  int64_t n = 0;
+  for (int rt = 0; rt < tiles; ++rt) n += units_of(s.end(a, group, rows, rt));
+  return n;
+}
+
+// Where a thread block's share of the list begins, and how long the list is.
+struct Share {
+  int64_t b;          // sequence of the share's first unit
+  int64_t off;        // the unit's place among the sequence's
+  int64_t lo, hi, total;
+  int blocks;         // how many blocks have a share that is not empty: the first ones
+};
+
+// All THREADS threads; scratch: THREADS / 32 values.  Each thread sums a run of sequences; the one
+// whose run holds the share's first unit walks it again.
+template <int THREADS>
+__device__ __forceinline__ void find_share(const AttnArgs& a, int group, int rows, int cta, int ctas,
+                                           int64_t* scratch, Share* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per = (a.batch + THREADS - 1) / THREADS;
+  const int64_t b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+  int64_t sum = 0;
+  for (int64_t b = b0; b < b1; ++b) sum += head_units(a, b, group, rows) * a.c.kv_heads;
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  // (a list of 2^52 units, where the product would not fit, would take years)
+  const int n = (int)min((int64_t)ctas, total);
+  const int64_t lo = cta < n ? total * cta / n : total, hi = cta < n ? total * (cta + 1) / n : total;
+  const int64_t first = before + incl - sum;
+  if (lo < hi && lo >= first && lo < first + sum) {
+    int64_t at = lo - first, b = b0;
+    for (; b < b1; ++b) {
+      const int64_t m = head_units(a, b, group, rows) * a.c.kv_heads;
+      if (at < m) break;
+      at -= m;
+    }
+    *out = {b, at, lo, hi, total, n};
+  }
+  if (tid == 0 && lo >= hi) *out = {0, 0, 0, 0, total, n};  // an empty share
+  __syncthreads();
+}
+
+// The block that unit u belongs to (the inverse of find_share's split).
+__device__ __forceinline__ int block_of(int64_t u, const Share& sh) {
+  return (int)(((u + 1) * sh.blocks - 1) / sh.total);
+}
+
+// A walk over the pieces of a share.
+struct Walk {
+  int64_t b;
+  int h, rt;           // segment
+  int c0, c1, n;       // its units of this share, and all of them
+  int end;             // positions the tile sees at most
+  int64_t left;        // units of the share behind this piece
+  int64_t u0;          // the list's place of the segment's first unit
+  __device__ __forceinline__ void set(const AttnArgs& a, int group, int rows, const Seq& s,
+                                      int first) {
+    end = s.end(a, group, rows, rt);
+    n = units_of(end);
+    c0 = first;
+    c1 = (int)min((int64_t)n, c0 + left);
+    left -= c1 - c0;
+  }
+  __device__ __forceinline__ void begin(const AttnArgs& a, int group, int rows, const Share& sh) {
+    b = sh.b;
+    const Seq s(a, b);
+    const int64_t per = head_units(a, b, group, rows);
+    h = (int)(sh.off / per);
+    int64_t at = sh.off - h * per;
+    rt = 0;
+    int m = units_of(s.end(a, group, rows, 0));
+    while (at >= m) {
+      at -= m;
+      m = units_of(s.end(a, group, rows, ++rt));
+    }
+    left = sh.hi - sh.lo;
+    u0 = sh.lo - at;
+    set(a, group, rows, s, (int)at);
+  }
+  // The next piece; only when left > 0.
+  __device__ __forceinline__ void next(const AttnArgs& a, int group, int rows) {
+    u0 += n;
+    if (++rt >= Seq(a, b).tiles(group, rows)) {
+      rt = 0;
+      if (++h >= a.c.kv_heads) {
+        h = 0;
+        do ++b;
+        while (Seq(a, b).tiles(group, rows) == 0);
+      }
+    }
+    set(a, group, rows, Seq(a, b), 0);
+  }
+  __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == n; }
+};
+
+// ---- workspace: one record per thread block, then two partial results per thread block ------------
+
+// Written by the block that holds a split segment's first units: the segment, and the blocks that
+// hold its pieces; last < 0: nothing to join.
+struct Record {
+  int64_t b;
+  int h, rt, last, pad;
+};
+static_assert(sizeof(Record) == 24, "record layout");
+
+// A partial result of up to R rows: R maxima (log2 domain), R sums, R x D outputs in float32.
+__host__ __device__ inline size_t partial_floats(int rows, int dim) {
+  return (size_t)rows * (dim + 2);
+}
+__host__ __device__ inline size_t records_bytes(int ctas) {
+  return ((size_t)ctas * sizeof(Record) + 255) / 256 * 256;
+}
+// Place 2 c holds block c's piece that begins inside a segment, place 2 c + 1 the one that begins
+// with a segment and does not end it.
+__device__ __forceinline__ float* partial(const AttnArgs& a, int ctas, int rows, int dim, int place) {
+  return reinterpret_cast<float*>(static_cast<char*>(a.workspace) + records_bytes(ctas)) +
+         (size_t)place * partial_floats(rows, dim);
+}
+
+// log2 of a power of two.
+__host__ __device__ constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+// ---- small helpers ---------------------------------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight E2M1 codes -> four f16 pairs, byte by byte.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Scales enter the products as f16 values S 2^-kScaleShift: with E4M3, E2M1 x S has at most 6
+// significant bits and lies in [2^-10, 2688]; with UE5M3, E2M1 x S 2^-4 in [2^-22, 46080], a multiple
+// of 2^-22.  Both are exact in f16 (subnormals included), so K and V enter the products exactly.
+template <int FMT>
+constexpr int kScaleShift = FMT == kUE5M3 ? 4 : 0;
+
+// f16 bits of a scale code, in both halves.
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_f16x2(int code) {
+  const float v = scale_value(code, FMT) * (FMT == kUE5M3 ? 0x1p-4f : 1.0f);
+  return pack_f16x2(v, v);
+}
+
+__device__ __forceinline__ int64_t row_offset(const Rows& x, int64_t b, int t, int head) {
+  return b * x.sb + (int64_t)t * x.st + (int64_t)head * x.sh;
+}
+
+// Whether the new token t (its tree word w) sees position pos < end.
+__device__ __forceinline__ bool sees(const AttnArgs& a, const Seq& s, int t, uint64_t w, int pos) {
+  const int j = pos - s.base;
+  return j < 0 || (a.tree ? j < s.count && ((w >> j) & 1) : j <= t);
+}
+
+}  // namespace attn
+}  // namespace mxk

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(const __grid_constant
   }
   const int log_chunks = __ffs(c.head_dim) - 5;  // 16-element chunks of a head
   const int n = c.kv_heads << (a.tile_shift + log_chunks);
-  const int log_block = __ffs(c.block) - 1, lanes = c.block >> 4;
+  const int lanes = c.block >> 4;
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_next();
   const int64_t first = a.start[b];
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(const __grid_constant
       if (!ok) continue;
       *reinterpret_cast<uint2*>(c.codes[s] + row * (c.head_dim >> 1) + 8 * it.chunk) = codes;
       if ((it.chunk & (lanes - 1)) == 0)
-        c.scales[s][row * (c.head_dim >> log_block) + ((16 * it.chunk) >> log_block)] = (uint8_t)sc;
+        c.scales[s][row * (c.head_dim >> c.log_block) + ((16 * it.chunk) >> c.log_block)] = (uint8_t)sc;
     }
   }
 }
@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__
   const float g[2] = {fp16_bits_to_float(c.g_bits[0]), fp16_bits_to_float(c.g_bits[1])};
   const int log_chunks = __ffs(c.head_dim) - 5;
   const int n = c.kv_heads << (a.tile_shift + log_chunks);
-  const int log_block = __ffs(c.block) - 1;
   griddep_wait();
   griddep_launch_next();
   const int64_t first = a.start[b];
@@ -191,8 +190,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__
       if (slot >= 0) {
         codes[s] = __ldg(reinterpret_cast<const uint2*>(c.codes[s] + row * (c.head_dim >> 1) +
                                                         8 * it.chunk));
-        sc[s] = __ldg(c.scales[s] + row * (c.head_dim >> log_block) +
-                      ((16 * it.chunk) >> log_block));
+        sc[s] = __ldg(c.scales[s] + row * (c.head_dim >> c.log_block) +
+                      ((16 * it.chunk) >> c.log_block));
       }
     }
 #pragma unroll

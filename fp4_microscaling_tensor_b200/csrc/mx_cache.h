@@ -15,6 +15,7 @@ struct CacheArgs {
   int64_t pages;
   int kv_heads, head_dim, block, fmt;
   int page_shift;      // log2(page_size)
+  int log_block;       // log2(block)
   uint16_t g_bits[2];
 };
 

@@ -1,104 +1,774 @@
 // mx_cache_attention.cu -- attention over a paged FP4 key/value cache.
 //
-// One warp per query row (sequence, token, head): 32 positions at a time, one per lane for the
-// scores, running maximum and sum of the softmax in fp32, head_dim / 32 output values per lane.
-#include "mx_cache.h"
-#include "mx_device.cuh"
+// out = softmax(scale q K^T) V with K = E2M1 S g as the cache stores them (microscaling article,
+// hotelren.com/news/2192771, §1 and §3.1 item 3), one pass over K and V with the running maximum m
+// and sum l of the softmax: for every chunk of positions, scores s = q K^T, m' = max(m, max s),
+// weights p = 2^((s - m') c), l = l 2^((m - m') c) + sum p, o = o 2^((m - m') c) + p V.
+//
+// k_attention_stream, for few query rows per key/value head (a decoder's steps, chains and small
+// trees of drafted tokens): what bounds it is reading the cache, 1 + 2 / N bytes per position and
+// head dimension, and next to it the instructions that turn codes into f16 (about 2 per pair of
+// codes), so both are what the layout is made for:
+//   * mma.sync m16n8k16 with the positions (scores) or the head dimension (outputs) as its 16 rows
+//     and the query rows as its 8 columns: 8 query rows -- 8 query heads that share a key/value head
+//     -- fill it.  The 128 lanes-deep tcgen05 tile would be 6 % full; the tensor pipe is not what
+//     bounds this.
+//   * the contraction index of a product may be permuted if both operands agree.  So a thread's part
+//     of the A operand of q K^T is a run of D / 4 consecutive codes of one position (16 bytes for D =
+//     128: one load, 1 or 2 scales), and its part of V^T is D / 8 consecutive codes of four positions.
+//     Two positions' codes are interleaved as nibbles (4 instructions per 16 codes) before they
+//     become f16 pairs along the positions, the layout the A operand of V^T p needs.
+//   * scores come out with positions in rows; movmatrix turns a pair of 8 x 8 weights tiles into the
+//     B operand of V^T p.  Nothing but codes and scales goes through shared memory.
+//   * every warp works for itself: cp.async brings its next tile (64 positions, keys and values, 8 KB
+//     + scales for D = 128) into a ring of its own while it computes; 12 warps per SM keep about 100
+//     KB in flight.  Bytes behind the end of the sequence, or of no page, arrive as zeros (a zero
+//     scale makes what the codes say harmless).
+// The warps of a block take the tiles of its piece in turn and join their results in shared memory at
+// the piece's end.
+#include <math.h>
+
+#include "mx_attention.cuh"
 #include "mx_launch.h"
 
 namespace mxk {
+namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
+// Position (0..15 of a tile's 16) that row i of an MMA stands for: rows 2 and 3, 6 and 7, ... change
+// places, so that the four lanes that read V at 2 t and 2 t + 1 hit both halves of 128 bytes.
+__device__ __forceinline__ int perm(int i) { return i ^ ((i >> 1) & 1); }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kWarps) k_cache_attention(const __grid_constant__ AttnArgs a) {
-  __shared__ float s_q[kWarps][D];
-  const CacheArgs& c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * kWarps + warp;
-  griddep_wait();
-  griddep_launch_next();
-  const int h = (int)(r % a.heads);
-  const int64_t bt = r / a.heads, b = bt / a.tokens, t = bt % a.tokens;
-  if (b >= a.batch) return;
-  const int64_t cnt = a.count ? min((int64_t)max(a.count[b], 0), a.tokens) : a.tokens;
-  if (t >= cnt) return;
-  const int64_t len = min((int64_t)max(a.length[b], 0), a.table.width << c.page_shift);
-  const int64_t base = len - cnt;
-  const uint16_t* q = static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + t * a.q.st + h * a.q.sh;
-  for (int i = lane; i < D; i += 32) s_q[warp][i] = __uint_as_float((uint32_t)q[i] << 16);
-  __syncwarp();
-  const uint64_t word = a.tree ? a.tree[b * a.tokens + t] : 0;
-  const int kvh = h / (a.heads / c.kv_heads);
-  const float kscale = a.scale * fp16_bits_to_float(c.g_bits[0]);
-  const int64_t end = a.tree ? len : min(len, base + t + 1);
-  float m = -INFINITY, l = 0.0f, acc[D / 32];
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-  for (int64_t p0 = 0; p0 < end; p0 += 32) {
-    const int64_t p = p0 + lane;
-    const int64_t j = p - base;
-    const bool seen = p < end && (!a.tree || j < 0 || ((word >> j) & 1));
-    int64_t row = p < end ? a.table.slot(c, b, p) : -1;
-    if (row >= 0) row += (int64_t)kvh << c.page_shift;
-    float s = -INFINITY;
-    if (seen && row >= 0) {
-      s = 0.0f;
-      for (int i = 0; i < D; i += 2) {
-        const uint32_t cw = c.codes[0][row * (D / 2) + i / 2];
-        const float S = scale_value(c.scales[0][row * (D / c.block) + i / c.block], FMT);
-        s += (e2m1_to_float(cw & 15u) * s_q[warp][i] + e2m1_to_float(cw >> 4) * s_q[warp][i + 1]) * S;
+constexpr int kWarps = 4;
+constexpr int kStreamThreads = 32 * kWarps;
+
+template <int D, int NT>
+struct Geometry {
+  // positions per tile: fewer where the accumulators leave few registers for the scores
+  static constexpr int kTile = D == 256 || NT == 4 ? 32 : 64;
+  static constexpr int kRow = D / 2;                       // code bytes of a position
+  static constexpr int kCodes = kTile * kRow;              // bytes of a tile's key (value) codes
+  static constexpr int kScales = kTile * (D / 16);         // most scale bytes of a tile's keys
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int kWarpBytes = 18432;                 // of shared memory
+  static constexpr int kStages = kWarpBytes / kStage;
+  // blocks per SM: registers for D NT / 4 accumulators and D NT / 8 words of queries
+  static constexpr int kBlocks = D * NT <= 128 ? 3 : 2;
+  static constexpr int kJoinPitch = D + 4;                 // floats per row when warps join
+};
+
+template <int D, int NT>
+constexpr int stream_smem() {
+  // rings, and behind them the scale table; the warps' results reuse their rings
+  static_assert(NT * 8 * Geometry<D, NT>::kJoinPitch * 4 <= Geometry<D, NT>::kWarpBytes, "join buffers");
+  return kWarps * Geometry<D, NT>::kWarpBytes;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* v) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint16_t v;
+  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u8 t, [%1];\n\tmov.b16 %0, t;\n\t}"
+               : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+      "%9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// Two scale codes (bytes 0 and 1 of w) -> f16 pair, times 2^-kScaleShift.  E4M3 by the hardware's
+// conversion.  UE5M3 has binary16's exponent: the code shifted to bits 7..14 is its value, except that
+// exponent 31 would be infinity.  Scaled by 2^-4 two ways -- a multiply, right below exponent 16 where
+// the shifted code loses its top exponent bit to the mask, and subtracting 4 from the exponent, right
+// from 5 on -- the larger one is the value: below 5 the second is negative or NaN, above 15 the first
+// is too small.
+template <int FMT>
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t w) {
+  uint32_t d;
+  if constexpr (FMT == kE4M3) {
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(w));
+  } else {
+    const uint32_t x = __byte_perm(w, 0, 0x4140) << 7;
+    const uint32_t low = mul_f16x2(x & 0x3FFF3FFFu, 0x2C002C00u);
+    const uint32_t high = ((x | 0x80008000u) - 0x10001000u) ^ 0x80008000u;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(low), "r"(high));
+  }
+  return d;
+}
+
+// One warp's tile ring, accumulators and softmax state for NT groups of 8 query rows.
+template <int D, int NT, int FMT, bool N16>
+struct Stream {
+  using G = Geometry<D, NT>;
+  static constexpr int KS = D / 16;               // k steps of q K^T
+  static constexpr int KB = D / 8;                // code bytes of a lane's run of a key
+  static constexpr int VB = D / 16;               // code bytes of a lane's run of a value
+  static constexpr int MT = D / 16;               // 16-row tiles of the outputs
+
+  const AttnArgs& a;
+  const int lane, g, t4;
+  const uint32_t ring;                            // shared address of the warp's ring
+  const int log_sb;                               // log2 of the scale bytes of a position
+
+  uint32_t q[NT][KS][2];                          // B operand of q K^T (f16 pairs)
+  float mult[NT][2];                              // log2 weight per unit of raw score, this lane's
+                                                  // two columns (query rows 8 nt + 2 t4, + 1)
+  float m[NT][2], l[NT][2];                       // running maximum (raw scores), partial sum
+  float o[NT][MT][4];
+
+  // segment
+  int64_t b;
+  int h, group, row0;
+  int end;                                        // positions of the piece (exclusive)
+  Seq seq;
+  int tok[NT][2];                                 // this lane's columns: token, and its tree word
+  uint64_t word[NT][2];
+
+  __device__ __forceinline__ Stream(const AttnArgs& args, uint32_t ring_addr)
+      : a(args), lane(threadIdx.x & 31), g(lane >> 2), t4(lane & 3), ring(ring_addr),
+        log_sb(log2_of(D) - args.c.log_block), seq(args, 0) {}
+
+  // Query rows row0 .. row0 + 8 NT - 1 of the segment: f16, each row scaled by the power of two that
+  // brings its largest magnitude to [2^14, 2^15) (exact for all values within 2^-28 of it; what is
+  // lost of smaller ones is below 2^-39 of it).
+  __device__ __forceinline__ void load_queries() {
+    const int rows = seq.count * group;
+    const float gk = fp16_bits_to_float(a.c.g_bits[0]) * (float)(1 << kScaleShift<FMT>);
+    const float base = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * gk * 1.4426950408889634f;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + 8 * nt + g;
+      uint32_t w[2 * KS];  // bf16 pairs
+      const bool in = r < rows && a.scale != 0.0f;
+      const int64_t at = in ? row_offset(a.q, b, r / group, h * group + r % group) : 0;
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        // run i of 16 bytes: values D <= 128: (D / 4) t4 + 8 i; D = 256: two runs of 32, 128 apart
+        const int d = D == 256 ? 128 * (i >> 2) + 32 * t4 + 8 * (i & 3) : (D / 4) * t4 + 8 * i;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + at + d));
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
       }
-      s *= kscale;
-    }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx);
-    const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet (or only NaN scores)
-    const float w = expf(s - mu), f = expf(m - mu);
-    float sum = w;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * f + sum;
-    m = mn;
-    for (int i = 0; i < D / 32; ++i) acc[i] *= f;
-    for (int k = 0; k < 32; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const int64_t rk = __shfl_sync(0xffffffffu, row, k);
-      if (wk == 0.0f || rk < 0) continue;
-      for (int i = 0; i < D / 32; ++i) {
-        const int d = lane + 32 * i;
-        const uint32_t cw = c.codes[1][rk * (D / 2) + d / 2];
-        const float S = scale_value(c.scales[1][rk * (D / c.block) + d / c.block], FMT);
-        acc[i] += wk * (e2m1_to_float((cw >> (4 * (d & 1))) & 15u) * S);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^f; an all-zero row and one with infinities or NaN stay as they are
+      const int f = mx == 0 || mx >= 0x7F80u ? 0 : 141 - max((int)(mx >> 7), 1);
+      const int f1 = f / 2, f2 = f - f1;  // |f| may be 140: two steps
+      const float s1 = __uint_as_float((uint32_t)(127 + f1) << 23);
+      const float s2 = __uint_as_float((uint32_t)(127 + f2) << 23);
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i)
+        q[nt][i >> 1][i & 1] =
+            pack_f16x2(bf16lo(w[i]) * s1 * s2, bf16hi(w[i]) * s1 * s2) ^ (in ? flip : 0u);
+      const float mine = base * __uint_as_float((uint32_t)(127 - f1) << 23) *
+                         __uint_as_float((uint32_t)(127 - f2) << 23);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // kept normal: a masked score times it stays -infinity
+        mult[nt][e] =
+            fminf(fmaxf(__shfl_sync(0xffffffffu, mine, 4 * (2 * t4 + e)), 0x1p-126f), 0x1p126f);
+        const int c = row0 + 8 * nt + 2 * t4 + e;
+        tok[nt][e] = c < rows ? c / group : 0;
+        word[nt][e] = c < rows && a.tree ? a.tree[b * a.tokens + tok[nt][e]] : 0;
       }
     }
   }
-  const float f = l == 0.0f ? 0.0f : fp16_bits_to_float(c.g_bits[1]) / l;
-  __nv_bfloat16* out =
-      static_cast<__nv_bfloat16*>(a.out.p) + b * a.out.sb + t * a.out.st + h * a.out.sh;
-  for (int i = 0; i < D / 32; ++i) out[lane + 32 * i] = __float2bfloat16_rn(acc[i] * f);
-  if (a.lse && lane == 0) a.lse[bt * a.heads + h] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + logf(l);
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
+    }
+  }
+
+  // Lane i < tile / 16 gets the row of the cache (in units of slots of one head) where the tile's
+  // 16 positions from p + 16 i on begin, or -1.  (Pages are whole multiples of 16 slots.)
+  __device__ __forceinline__ int64_t page_rows(int p, int groups) const {
+    const int64_t pos = (int64_t)p + 16 * lane;
+    int64_t row = -1;
+    if (lane < groups && pos < end) {
+      row = a.table.slot(a.c, b, pos);
+      if (row >= 0) row += (int64_t)h << a.c.page_shift;
+    }
+    return row;
+  }
+
+  // Issues the copies of the TS positions from p on into slot `stage` of the ring.
+  template <int TS>
+  __device__ __forceinline__ void issue(int p, int64_t rows, int stage) {
+    constexpr int CH = D / 32;          // 16-byte pieces of a position's codes
+    constexpr int IT = TS * D / 1024;   // pieces per lane
+    const uint32_t st = ring + stage * G::kStage;
+    const int piece = lane % CH;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int i = (32 / CH) * k + lane / CH;  // position in the tile
+      const int64_t row = __shfl_sync(0xffffffffu, rows, (32 / CH) * k / 16);
+      const bool ok = row >= 0 && p + i < end;
+      const int64_t at = ok ? (row + (i & 15)) * G::kRow + 16 * piece : 0;
+      uint32_t kd, vd;
+      if constexpr (D == 64) {
+        kd = 32 * i + 16 * piece;
+        vd = 32 * (i ^ ((i >> 2) & 1)) + 16 * piece;
+      } else if constexpr (D == 128) {
+        kd = 64 * i + 16 * piece;
+        vd = 64 * i + 16 * (piece ^ ((i >> 1) & 3));
+      } else {
+        kd = 128 * i + 16 * (piece ^ ((i & 1) << 2));
+        vd = 128 * i + 16 * (piece ^ (((i >> 1) & 3) << 1));
+      }
+      cp_async16(st + kd, a.c.codes[0] + at, ok ? 16 : 0);
+      cp_async16(st + G::kCodes + vd, a.c.codes[1] + at, ok ? 16 : 0);
+    }
+    // scales: 16 positions hold 16 << log_sb contiguous bytes; a piece covers 16 >> log_sb positions
+    const int i = (lane >> log_sb) * 16 + ((lane & ((1 << log_sb) - 1)) << (4 - log_sb));
+    const int64_t row = __shfl_sync(0xffffffffu, rows, (lane >> log_sb) & 3);
+    if (lane < (TS / 16 << log_sb)) {
+      const int n = row >= 0 ? min(max(end - (p + i), 0), 16 >> log_sb) << log_sb : 0;
+      const int64_t at = n ? (row + (i & 15)) << log_sb : 0;
+      cp_async16(st + 2 * G::kCodes + (i << log_sb), a.c.scales[0] + at, n);
+      cp_async16(st + 2 * G::kCodes + G::kScales + (i << log_sb), a.c.scales[1] + at, n);
+    }
+    cp_commit();
+  }
+
+  // The TS positions from p on, in slot `stage`; rows: their page_rows.
+  template <int TS>
+  __device__ __forceinline__ void compute(int p, int64_t rows, int stage) {
+    constexpr int T = TS / 16;
+    const uint32_t kc = ring + stage * G::kStage, vc = kc + G::kCodes, ks = vc + G::kCodes,
+                   vs = ks + G::kScales;
+    const int log_block = a.c.log_block;
+    float s[NT][T][4];
+    // ---- scores
+#pragma unroll
+    for (int mt = 0; mt < T; ++mt) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][mt][e] = 0.0f;
+      const int ia = 16 * mt + perm(g);  // and ia + 8
+      constexpr int RUNS = D == 256 ? 2 : 1;       // runs of 32 (D = 64: 16) codes
+      constexpr int RB = KB / RUNS;                // bytes of a run
+#pragma unroll
+      for (int run = 0; run < RUNS; ++run) {
+        uint32_t c[2][RB / 4], sc[2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = ia + 8 * e;
+          const uint32_t piece = D == 256 ? (uint32_t)((t4 + 4 * run) ^ ((i & 1) << 2)) : (uint32_t)t4;
+          lds<RB>(kc + i * G::kRow + piece * RB, c[e]);
+          const uint32_t d0 = D == 256 ? 128 * run + 32 * t4 : (D / 4) * t4;
+          const uint32_t sa = ks + (i << log_sb) + (d0 >> log_block);
+          if constexpr (N16 && RB == 16) {  // two scales: 16 codes each
+            const uint32_t f = scales_f16x2<FMT>(lds_u16(sa));
+            sc[e][0] = __byte_perm(f, f, 0x1010);
+            sc[e][1] = __byte_perm(f, f, 0x3232);
+          } else {
+            const uint32_t w = lds_u8(sa);
+            sc[e][0] = sc[e][1] = scales_f16x2<FMT>(w | (w << 8));
+          }
+        }
+#pragma unroll
+        for (int wd = 0; wd < RB / 4; ++wd) {
+          uint32_t ha[4], hb[4];
+          e2m1x8_to_f16(c[0][wd], ha);
+          e2m1x8_to_f16(c[1][wd], hb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ha[i] = mul_f16x2(ha[i], sc[0][(N16 && RB == 16) ? wd >> 1 : 0]);
+            hb[i] = mul_f16x2(hb[i], sc[1][(N16 && RB == 16) ? wd >> 1 : 0]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t f[4] = {ha[2 * e], hb[2 * e], ha[2 * e + 1], hb[2 * e + 1]};
+            const int k = (RB / 2) * run + 2 * wd + e;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(s[nt][mt], f, q[nt][k][0], q[nt][k][1]);
+          }
+        }
+      }
+    }
+    // ---- masks: only tiles with new tokens, the end, or positions without a page
+    const uint32_t have = __ballot_sync(0xffffffffu, rows >= 0);
+    if (p + TS > min(end, seq.base + 1) || (have & ((1u << T) - 1)) != (1u << T) - 1) {
+#pragma unroll
+      for (int mt = 0; mt < T; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int pos = p + 16 * mt + 8 * half + perm(g);
+          const bool in = pos < end && ((have >> mt) & 1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!in || !sees(a, seq, tok[nt][e], word[nt][e], pos))
+                s[nt][mt][2 * half + e] = -INFINITY;
+        }
+    }
+    // ---- running maximum and weights
+    uint32_t pb[NT][T][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mu[2];
+      bool grew = false;
+      float alpha[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(s[nt][0][e], s[nt][0][2 + e]);
+#pragma unroll
+        for (int mt = 1; mt < T; ++mt) mx = fmaxf(mx, fmaxf(s[nt][mt][e], s[nt][mt][2 + e]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m[nt][e], mx);
+        grew |= mn > m[nt][e];
+        mu[e] = mn == -INFINITY ? 0.0f : mn * mult[nt][e];
+        alpha[e] = m[nt][e] == -INFINITY ? 0.0f : ex2((m[nt][e] - mn) * mult[nt][e]);
+        m[nt][e] = mn;
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (m[nt][e] == -INFINITY) alpha[e] = 1.0f;  // nothing seen yet: nothing to scale
+          l[nt][e] *= alpha[e];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][i][e] *= alpha[e & 1];
+      }
+#pragma unroll
+      for (int mt = 0; mt < T; ++mt) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = ex2(fmaf(s[nt][mt][e], mult[nt][e & 1], -mu[e & 1]));
+          l[nt][e & 1] += w[e];
+        }
+        // binary16 weights, at most 1: 2^-11 each, and 2^-25 below the normal range
+        pb[nt][mt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+        pb[nt][mt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+      }
+    }
+    // ---- outputs: V^T p
+#pragma unroll
+    for (int kt = 0; kt < T; ++kt) {
+      uint32_t c[4][VB / 4 > 0 ? VB / 4 : 1];
+      uint32_t sc[2][2];  // [position pair][half of the lane's run]
+      uint32_t sw[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * kt + 8 * (e >> 1) + perm(2 * t4 + (e & 1));
+        uint32_t at;
+        if constexpr (D == 64) at = 32 * (i ^ ((i >> 2) & 1)) + 4 * g;
+        else if constexpr (D == 128) at = 64 * i + 16 * ((g >> 1) ^ ((i >> 1) & 3)) + 8 * (g & 1);
+        else at = 128 * i + 16 * (g ^ (((i >> 1) & 3) << 1));
+        lds<VB>(vc + at, c[e]);
+        const uint32_t sa = vs + (i << log_sb) + ((uint32_t)(g * (D / 8)) >> log_block);
+        sw[e] = (N16 && D == 256) ? lds_u16(sa) : lds_u8(sa);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sc[e][0] = scales_f16x2<FMT>(__byte_perm(sw[2 * e], sw[2 * e + 1], 0x0040));
+        sc[e][1] = (N16 && D == 256)
+                       ? scales_f16x2<FMT>(__byte_perm(sw[2 * e], sw[2 * e + 1], 0x0051))
+                       : sc[e][0];
+      }
+#pragma unroll
+      for (int wd = 0; wd < VB / 4; ++wd) {
+        uint32_t ev[2][4], od[2][4];  // even and odd codes of the word: pairs of positions
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = c[2 * e][wd], y = c[2 * e + 1][wd];
+          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[e]);
+          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[e]);
+          const uint32_t f = sc[e][VB / 4 == 4 ? wd >> 1 : 0];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ev[e][i] = mul_f16x2(ev[e][i], f);
+            od[e][i] = mul_f16x2(od[e][i], f);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t f[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * wd + i], f, pb[nt][kt][0], pb[nt][kt][1]);
+        }
+      }
+    }
+  }
+
+  // The tiles first, first + step, ... of TS positions of [p0, end).
+  template <int TS>
+  __device__ __forceinline__ void run(int p0, int first, int step) {
+    constexpr int S = G::kStages;
+    const int tiles = (end - p0 + TS - 1) / TS;
+    int64_t rows[S];  // page rows of the tiles in the ring
+#pragma unroll
+    for (int s = 0; s < S; ++s) rows[s] = -1;
+    int64_t ahead = page_rows(p0 + first * TS, TS / 16);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) {
+      const int i = first + s * step;
+      rows[s] = ahead;
+      if (i < tiles) issue<TS>(p0 + i * TS, ahead, s);
+      else cp_commit();
+      ahead = i + step < tiles ? page_rows(p0 + (i + step) * TS, TS / 16) : -1;
+    }
+    for (int base = first; base < tiles; base += S * step) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const int i = base + s * step;
+        if (i >= tiles) break;
+        const int next = i + (S - 1) * step;
+        rows[(s + S - 1) % S] = ahead;
+        if (next < tiles) issue<TS>(p0 + next * TS, ahead, (s + S - 1) % S);
+        else cp_commit();
+        ahead = next + step < tiles ? page_rows(p0 + (next + step) * TS, TS / 16) : -1;
+        cp_wait<S - 1>();
+        __syncwarp();
+        compute<TS>(p0 + i * TS, rows[s], s);
+        __syncwarp();
+      }
+    }
+    cp_wait<0>();
+    __syncwarp();
+  }
+};
+
+// Result of a piece: rows x D outputs (unnormalised, relative to the maximum), joined over the
+// block's warps.  out/lse, or a partial result.
+template <int D, int NT, int FMT, bool N16>
+__global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
+    k_attention_stream(const __grid_constant__ AttnArgs a) {
+  using G = Geometry<D, NT>;
+  constexpr int R = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ Share s_share;
+  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
+  griddep_wait();
+  griddep_launch_next();
+  find_share<kStreamThreads>(a, group, R, cta, ctas, s_scan, &s_share);
+  const Share sh = s_share;
+  Record* rec = reinterpret_cast<Record*>(a.workspace) + cta;
+  Record mine{0, 0, 0, -1, 0};
+  const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
+
+  if (sh.lo < sh.hi) {
+    Stream<D, NT, FMT, N16> w(a, smem_addr(smem) + warp * G::kWarpBytes);
+    w.group = group;
+    Walk k;
+    k.begin(a, group, R, sh);
+    while (true) {
+      w.b = k.b;
+      w.h = k.h;
+      w.row0 = k.rt * R;
+      w.seq = Seq(a, k.b);
+      const int p0 = k.c0 * kUnit;
+      w.end = min(k.end, k.c1 * kUnit);
+      w.load_queries();
+      w.reset();
+      // long pieces: a tile per warp in turn; short ones: 16 positions per warp
+      if (w.end - p0 >= kWarps * G::kTile) w.template run<G::kTile>(p0, warp, kWarps);
+      else w.template run<16>(p0, warp, kWarps);
+
+      // join the warps: maxima first
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float l = w.l[nt][e];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+          if (w.g == 0) {
+            const int r = 8 * nt + 2 * w.t4 + e;
+            s_m[warp][r] = w.m[nt][e] * w.mult[nt][e];  // (-inf stays)
+            s_l[warp][r] = l;
+          }
+        }
+      // this warp's outputs into its own ring
+      float* mine_o = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(mine_o + (8 * nt + 2 * w.t4 + e) * G::kJoinPitch +
+                                       (D / 8) * w.g + 2 * i) =
+                make_float2(w.o[nt][i][e], w.o[nt][i][2 + e]);
+      __syncthreads();
+
+      const int rows = min(R, w.seq.count * group - w.row0);
+      const bool whole = k.whole();
+      float* part = partial(a, ctas, R, D, 2 * cta + (k.c0 == 0));
+      for (int i = threadIdx.x; i < R * (D / 8); i += kStreamThreads) {
+        const int r = i / (D / 8), d = 8 * (i % (D / 8));
+        if (r >= rows) break;
+        float mx = s_m[0][r];
+#pragma unroll
+        for (int x = 1; x < kWarps; ++x) mx = fmaxf(mx, s_m[x][r]);
+        const float mu = mx == -INFINITY ? 0.0f : mx;
+        float l = 0.0f, y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float f = ex2(s_m[x][r] - mu);
+          l += s_l[x][r] * f;
+          const float* src = reinterpret_cast<const float*>(smem + x * G::kWarpBytes) +
+                             r * G::kJoinPitch + d;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] += src[e] * f;
+        }
+        if (whole) {
+          const int row = w.row0 + r, t = row / group, head = k.h * group + row % group;
+          const float f = l == 0.0f ? 0.0f : gv / l;
+          const uint4 v = make_uint4(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f),
+                                     pack_bf16x2(y[4] * f, y[5] * f), pack_bf16x2(y[6] * f, y[7] * f));
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out.p) +
+                                    row_offset(a.out, k.b, t, head) + d) = v;
+          if (a.lse && d == 0)
+            a.lse[(k.b * a.tokens + t) * a.heads + head] =
+                l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+        } else {
+          float4* dst = reinterpret_cast<float4*>(part + 2 * R + r * D + d);
+          dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+          dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+          if (d == 0) part[r] = mx, part[R + r] = l;
+        }
+      }
+      if (k.c0 == 0 && !whole) mine = {k.b, k.h, k.rt, block_of(k.u0 + k.n - 1, sh), 0};
+      __syncthreads();
+      if (k.left <= 0) break;
+      k.next(a, group, R);
+    }
+  }
+  if (threadIdx.x == 0) *rec = mine;
+}
+
+// Joins the pieces of the segment that block blockIdx.x began and did not end: blocks c .. last hold
+// one each.  blockIdx.y: a quarter of the head dimension.  A thread holds four outputs of a row and
+// every K-th piece; the K runs are added up in order.
+template <int D, int R>
+__global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ AttnArgs a, int ctas,
+                                                        float gv) {
+  constexpr int kItems = R * (D / 16);               // float4 outputs of a quarter
+  constexpr int kPer = kItems < 256 ? kItems : 256;  // threads per run
+  constexpr int K = 256 / kPer;
+  __shared__ float4 s_o[K][kPer];
+  __shared__ float s_m[K][kPer], s_l[K][kPer];
+  griddep_wait();
+  griddep_launch_next();
+  const int c = blockIdx.x;
+  const Record rec = reinterpret_cast<const Record*>(a.workspace)[c];
+  if (rec.last < 0) return;
+  const int group = a.heads / a.c.kv_heads;
+  const int count = a.count ? (int)min((int64_t)max(a.count[rec.b], 0), a.tokens) : (int)a.tokens;
+  const int rows = min((int64_t)R, (int64_t)count * group - (int64_t)rec.rt * R);
+  const int n = rec.last - c + 1;
+  for (int i0 = 0; i0 < kItems; i0 += kPer) {
+    const int i = i0 + (int)threadIdx.x % kPer, run = threadIdx.x / kPer;
+    const int r = i / (D / 16), d = blockIdx.y * (D / 4) + 4 * (i % (D / 16));
+    float mx = -INFINITY, l = 0.0f;
+    float4 y = make_float4(0, 0, 0, 0);
+    if (r < rows) {
+      // pieces run * per .. : an order that depends on their number only
+      const int per = (n + K - 1) / K, x1 = min(n, (run + 1) * per);
+      for (int x0 = run * per; x0 < x1; x0 += 4) {
+        float pm[4], pl[4];
+        float4 po[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pm[e] = -INFINITY, pl[e] = 0.0f, po[e] = make_float4(0, 0, 0, 0);
+          if (x0 + e < x1) {
+            const float* p = partial(a, ctas, R, D, 2 * (c + x0 + e) + (x0 + e == 0));
+            pm[e] = p[r], pl[e] = p[R + r];
+            po[e] = *reinterpret_cast<const float4*>(p + 2 * R + r * D + d);
+          }
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mx);
+        const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(mx - mu);
+        l *= f, y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+        mx = mn;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = ex2(pm[e] - mu);
+          l += pl[e] * w;
+          y.x += po[e].x * w, y.y += po[e].y * w, y.z += po[e].z * w, y.w += po[e].w * w;
+        }
+      }
+    }
+    if constexpr (K > 1) {
+      const int j = threadIdx.x % kPer;
+      s_m[run][j] = mx, s_l[run][j] = l, s_o[run][j] = y;
+      __syncthreads();
+      if (run == 0) {
+        float mn = mx;
+#pragma unroll
+        for (int x = 1; x < K; ++x) mn = fmaxf(mn, s_m[x][j]);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        l = 0.0f, y = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < K; ++x) {
+          const float w = ex2(s_m[x][j] - mu);
+          const float4 v = s_o[x][j];
+          l += s_l[x][j] * w;
+          y.x += v.x * w, y.y += v.y * w, y.z += v.z * w, y.w += v.w * w;
+        }
+        mx = mn;
+      }
+    }
+    if (r < rows && run == 0) {
+      const int64_t row = (int64_t)rec.rt * R + r;
+      const int t = (int)(row / group), head = rec.h * group + (int)(row % group);
+      const float f = l == 0.0f ? 0.0f : gv / l;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + row_offset(a.out, rec.b, t, head) +
+                                d) =
+          make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+      if (a.lse && d == 0)
+        a.lse[(rec.b * a.tokens + t) * a.heads + head] =
+            l == 0.0f ? -INFINITY
+                      : ((mx == -INFINITY ? 0.0f : mx) + log2f(l)) * 0.6931471805599453f;
+    }
+    if constexpr (K > 1) __syncthreads();
+  }
+}
+
+// Query rows per tile: 8, 16 or 32, as many as there are (a tile's rows share one pass over the
+// cache); 16 at most for head_dim 256, whose accumulators fill the registers.
+int row_tiles(int64_t rows, int dim) {
+  const int most = dim == 256 ? 2 : 4;
+  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  return nt < most ? nt : most;
+}
+
+constexpr int kMaxStreamCtas = 3 * 160;  // thread blocks at most: 3 per SM
+
+template <int D, int NT, int FMT, bool N16>
+cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  static std::atomic<bool> attr[kMaxDevices];
+  constexpr int smem = stream_smem<D, NT>();
+  auto* kern = k_attention_stream<D, NT, FMT, N16>;
+  cudaError_t e = allow_dynamic_smem(attr, kern, smem);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int per_sm = Geometry<D, NT>::kBlocks;
+  // never more blocks than units that the table could hold
+  const int group = a.heads / a.c.kv_heads;
+  const int64_t tiles = (a.tokens * group + 8 * NT - 1) / (8 * NT);
+  const int64_t reach = (a.table.width << a.c.page_shift) / kUnit + 1;
+  int64_t grid = (int64_t)per_sm * (sms < 160 ? sms : 160);
+  const double most = (double)a.batch * a.c.kv_heads * tiles * reach;
+  if (most < (double)grid) grid = (int64_t)most;
+  const int ctas = (int)(grid < 1 ? 1 : grid);
+  e = launch_pdl_smem(kern, ctas, kStreamThreads, smem, stream, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  // the join: its blocks only read a record where nothing was split
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 4);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  uint32_t gb = a.c.g_bits[1];
+  const float gv = (gb >> 10 ? (1024 + (gb & 1023)) * exp2f((float)(gb >> 10) - 25.0f)
+                             : gb * 0x1p-24f) * (float)(1 << kScaleShift<FMT>);
+  e = cudaLaunchKernelEx(&cfg, k_attention_join<D, 8 * NT>, a, ctas, gv);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+template <int D, int NT>
+cudaError_t dispatch_format(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  if (a.c.fmt == kUE5M3)
+    return a.c.block == 16 ? launch_stream<D, NT, kUE5M3, true>(a, stream, launches)
+                           : launch_stream<D, NT, kUE5M3, false>(a, stream, launches);
+  return a.c.block == 16 ? launch_stream<D, NT, kE4M3, true>(a, stream, launches)
+                         : launch_stream<D, NT, kE4M3, false>(a, stream, launches);
 }
 
 template <int D>
-cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  const int64_t grid = (a.batch * a.tokens * a.heads + kWarps - 1) / kWarps;
-  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  return a.c.fmt == kUE5M3
-             ? launch_pdl(k_cache_attention<D, kUE5M3>, (int)grid, 32 * kWarps, stream, a)
-             : launch_pdl(k_cache_attention<D, kE4M3>, (int)grid, 32 * kWarps, stream, a);
+cudaError_t dispatch_rows(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  const int nt = row_tiles(a.tokens * (a.heads / a.c.kv_heads), D);
+  if (nt == 1) return dispatch_format<D, 1>(a, stream, launches);
+  if constexpr (D < 256) {
+    if (nt == 4) return dispatch_format<D, 4>(a, stream, launches);
+  }
+  return dispatch_format<D, 2>(a, stream, launches);
 }
 
 }  // namespace
+}  // namespace attn
 
-size_t attention_workspace_bytes(int64_t, int64_t, int, int, int) { return 16; }
+size_t attention_workspace_bytes(int64_t batch, int64_t tokens, int heads, int kv_heads,
+                                 int head_dim) {
+  if (batch == 0 || tokens == 0) return 16;
+  const int rows = 8 * attn::row_tiles(tokens * (heads / kv_heads), head_dim);
+  return attn::records_bytes(attn::kMaxStreamCtas) +
+         2 * (size_t)attn::kMaxStreamCtas * attn::partial_floats(rows, head_dim) * 4;
+}
 
 cudaError_t run_cache_attention(const AttnArgs& a, cudaStream_t stream, int* launches) {
-  const cudaError_t e = a.c.head_dim == 64    ? launch<64>(a, stream)
-                        : a.c.head_dim == 128 ? launch<128>(a, stream)
-                                              : launch<256>(a, stream);
-  if (e == cudaSuccess) ++*launches;
-  return e;
+  switch (a.c.head_dim) {
+    case 64: return attn::dispatch_rows<64>(a, stream, launches);
+    case 128: return attn::dispatch_rows<128>(a, stream, launches);
+    default: return attn::dispatch_rows<256>(a, stream, launches);
+  }
 }
 
 }  // namespace mxk

@@ -394,7 +394,8 @@ MX_API size_t mx_cache_attention_workspace_size(int64_t batch, int64_t tokens, i
  *                  own bit is set): a tree of drafted tokens.  tokens <= 64 then.
  * A token that sees nothing gets zeros (and -infinity in lse).
  *   q      [batch, tokens, heads, head_dim], bf16; heads a multiple of cache->kv_heads, at most
- *          64 * kv_heads
+ *          64 * kv_heads, and tokens * heads / kv_heads < 2^31
+ *   max_pages  max_pages * page_size at most 2^30
  *   scale  finite; usually 1 / sqrt(head_dim)
  *   out    OUT [batch, tokens, heads, head_dim], bf16
  *   lse    OUT or NULL: the natural logarithm of the sum of the exponentials, float32,

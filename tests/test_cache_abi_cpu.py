@@ -110,6 +110,10 @@ def test_attention_arguments():
     assert attend(heads=7) == INV and attend(heads=0) == INV and attend(heads=-8) == INV
     assert attend(heads=2 * 65) == UNS
     assert attend(t=65, tree=A, n=1 << 40) == UNS
+    assert attend(t=1 << 30, heads=4, n=1 << 40) == UNS       # 2^31 query rows of a kv head
+    assert attend(w=(1 << 24) + 1, n=1 << 40) == UNS          # tables that reach beyond 2^30
+    arm()
+    assert stopped(attend(w=1 << 24))
     assert attend(scale=math.inf) == INV and attend(scale=math.nan) == INV
     assert attend(tree=A + 4) == MIS
     assert attend(lse=A + 2) == MIS
