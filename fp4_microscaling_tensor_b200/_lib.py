@@ -106,7 +106,7 @@ lib.mx_matmul_prepare_scales.restype = _i
 lib.mx_matmul_prepare_scales.argtypes = [_vp, _i64, _i64, _vp, _sz, _vp]
 lib.mx_matmul_gave_up.restype = _i
 lib.mx_matmul_gave_up.argtypes = [ctypes.POINTER(ctypes.c_uint)]
-Strides = _i64 * 3
+Strides = _i64 * 4  # a 4-D tensor's; the library reads the first three
 _cp, _st = ctypes.POINTER(Cache), ctypes.POINTER(_i64)
 lib.mx_cache_append.restype = _i
 lib.mx_cache_append.argtypes = [_cp, _vp, _vp, _i, _st, _st, _i64, _i64, _vp, _i64, _i64, _vp, _vp,

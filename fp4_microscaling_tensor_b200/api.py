@@ -5,9 +5,9 @@ Tensors are CUDA tensors, contiguous, row-major, with blocks along the last dime
 allocated with torch on the tensor's device unless given.  Calls are asynchronous on the current
 torch stream (or `stream=`); nothing here synchronizes except ErrorStats.to_dict().
 """
-import contextlib
 import ctypes
 import struct
+from contextlib import nullcontext
 
 import numpy as np
 import torch
@@ -507,28 +507,28 @@ class KVCache:
         self.fmt, self.device = fmt_code(fmt), k_codes.device
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_g, self.v_g = g_bits(k_g), g_bits(v_g)
+        self._workspaces = {}  # sizes by shape
         self._desc = Cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                            v_scales.data_ptr(), self.pages, self.kv_heads, self.page_size,
                            self.head_dim, self.block, self.fmt, self.k_g, self.v_g)
 
 
-def _strides(t):
-    """The first three strides of a [batch, tokens, heads, head_dim] tensor (0 where the dimension
-    has one entry: it is never stepped over)."""
-    return Strides(*(st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape[:3])))
+_CACHE_TYPES, _QUERY_TYPES = (torch.bfloat16, torch.float32), (torch.bfloat16,)
 
 
 def _outside(t, what, cache, dtypes, shape=None, written=False):
-    """Checks a [batch, tokens, heads, head_dim] tensor given to a cache call."""
+    """Checks a [batch, tokens, heads, head_dim] tensor given to a cache call; its strides."""
     if t.dim() != 4 or t.device != cache.device or t.dtype not in dtypes:
         raise ValueError(f"{what}: a 4-D tensor [batch, tokens, heads, head_dim] on the cache's "
                          f"device, {' or '.join(str(d).split('.')[1] for d in dtypes)}")
-    if t.shape[3] != cache.head_dim or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.shape[3] != cache.head_dim or (shape is not None and t.shape != shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)} does not fit")
-    if t.stride(3) != 1 or (written and any(n > 1 and st == 0
-                                            for n, st in zip(t.shape, t.stride()))):
+    strides = t.stride()
+    if strides[3] != 1 or (written and 0 in strides and
+                           any(n > 1 and st == 0 for n, st in zip(t.shape, strides))):
         raise ValueError(f"{what}: the last dimension contiguous"
                          + (", no dimension expanded" if written else ""))
+    return Strides(*strides)
 
 
 def _sequences(cache, batch, table, first, count, what):
@@ -547,27 +547,37 @@ def _sequences(cache, batch, table, first, count, what):
 
 
 def _allocating(stream):
-    """Where outputs and scratch are allocated (and zeroed): on the stream that uses them."""
-    if stream is None:
-        return contextlib.nullcontext()
+    """Where outputs and scratch are allocated (and zeroed) when the caller names a stream: there."""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(int(stream)))
 
 
-def _call(fn, where, device, *args):
-    """fn(*args) with the device current that the tensors live on."""
+# the current stream's handle without a Stream object around it (a decoder's step makes many small
+# calls: 0.1 us instead of 2)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) with the device current that the tensors live on."""
+    if stream is None and _raw_stream is not None:
+        stream = _raw_stream(device.index)
+    else:
+        stream = _stream(stream, device)
     if device.index == torch.cuda.current_device():
-        status = fn(*args)
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            status = fn(*args)
-    check(status, where)
+            status = fn(*args, stream)
+    if status:
+        check(status, where)
 
 
 def _new(shape, dtype, cache, count, stream):
     """A new output; zeros where a count may leave rows of it unwritten."""
+    make = torch.empty if count is None else torch.zeros
+    if stream is None:
+        return make(shape, dtype=dtype, device=cache.device)
     with _allocating(stream):
-        make = torch.empty if count is None else torch.zeros
         return make(shape, dtype=dtype, device=cache.device)
 
 
@@ -577,15 +587,14 @@ def cache_append(cache, k, v, table, start, count=None, stream=None):
     fused projection) becomes position start[b] + t of sequence b; codes and scales are those of
     quantize().  table int32 [batch, max_pages], start and count int32 [batch], on the device.
     Tokens behind count (padding) are not read; positions without a page are not written."""
-    _outside(k, "k", cache, (torch.bfloat16, torch.float32))
-    _outside(v, "v", cache, (k.dtype,), k.shape)
+    k_strides = _outside(k, "k", cache, _CACHE_TYPES)
+    v_strides = _outside(v, "v", cache, (k.dtype,), k.shape)
     if k.shape[2] != cache.kv_heads:
         raise ValueError(f"k: {cache.kv_heads} heads in the cache")
     batch, tokens = k.shape[:2]
     at = _sequences(cache, batch, table, start, count, "start")
-    _call(lib.mx_cache_append, "mx_cache_append", cache.device, cache._desc, k.data_ptr(),
-          v.data_ptr(), _DT[k.dtype], _strides(k), _strides(v), batch, tokens, *at,
-          _stream(stream, cache.device))
+    _call(lib.mx_cache_append, "mx_cache_append", cache.device, stream, cache._desc, k.data_ptr(),
+          v.data_ptr(), _DT[k.dtype], k_strides, v_strides, batch, tokens, *at)
 
 
 def cache_read(cache, table, start, count, tokens, out_dtype=torch.bfloat16, k_out=None, v_out=None,
@@ -599,19 +608,23 @@ def cache_read(cache, table, start, count, tokens, out_dtype=torch.bfloat16, k_o
         k_out = _new(shape, out_dtype if v_out is None else v_out.dtype, cache, count, stream)
     if v_out is None:
         v_out = _new(shape, k_out.dtype, cache, count, stream)
-    _outside(k_out, "k_out", cache, (torch.bfloat16, torch.float32), shape, written=True)
-    _outside(v_out, "v_out", cache, (k_out.dtype,), shape, written=True)
+    k_strides = _outside(k_out, "k_out", cache, _CACHE_TYPES, shape, written=True)
+    v_strides = _outside(v_out, "v_out", cache, (k_out.dtype,), shape, written=True)
     at = _sequences(cache, batch, table, start, count, "start")
-    _call(lib.mx_cache_read, "mx_cache_read", cache.device, cache._desc, *at, batch, int(tokens),
-          k_out.data_ptr(), v_out.data_ptr(), _DT[k_out.dtype], _strides(k_out), _strides(v_out),
-          _stream(stream, cache.device))
+    _call(lib.mx_cache_read, "mx_cache_read", cache.device, stream, cache._desc, *at, batch,
+          int(tokens), k_out.data_ptr(), v_out.data_ptr(), _DT[k_out.dtype], k_strides, v_strides)
     return k_out, v_out
 
 
-def attention_workspace(cache, batch, tokens, heads, device=None):
+def attention_workspace(cache, batch, tokens, heads):
     """Scratch for cache_attention() calls of this shape that do not run at the same time."""
-    n = lib.mx_cache_attention_workspace_size(batch, tokens, heads, cache.kv_heads, cache.head_dim)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device if device is None else device)
+    n = cache._workspaces.get((batch, tokens, heads))
+    if n is None:
+        n = lib.mx_cache_attention_workspace_size(batch, tokens, heads, cache.kv_heads,
+                                                  cache.head_dim)
+        if len(cache._workspaces) < 4096:
+            cache._workspaces[batch, tokens, heads] = n
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, out=None, lse=None,
@@ -629,7 +642,7 @@ def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, 
     or a float32 [batch, tokens, heads] tensor: the log of the sum of exponentials, -inf for a
     token that sees nothing.  Rows behind count keep what out and lse hold, or are zero in new
     tensors."""
-    _outside(q, "q", cache, (torch.bfloat16,))
+    q_strides = _outside(q, "q", cache, _QUERY_TYPES)
     batch, tokens, heads, dim = q.shape
     if heads < 1 or heads % cache.kv_heads:
         raise ValueError(f"q: a multiple of the cache's {cache.kv_heads} heads")
@@ -639,20 +652,19 @@ def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, 
         raise ValueError("tree: contiguous int64 [batch, tokens] on the cache's device")
     if out is None:
         out = _new(q.shape, torch.bfloat16, cache, count, stream)
-    _outside(out, "out", cache, (torch.bfloat16,), q.shape, written=True)
+    out_strides = _outside(out, "out", cache, _QUERY_TYPES, q.shape, written=True)
     if lse is True:
         lse = _new((batch, tokens, heads), torch.float32, cache, count, stream)
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (batch, tokens, heads)
                             or lse.device != cache.device or not lse.is_contiguous()):
         raise ValueError("lse: contiguous float32 [batch, tokens, heads] on the cache's device")
     if workspace is None:
-        with _allocating(stream):
+        with nullcontext() if stream is None else _allocating(stream):
             workspace = attention_workspace(cache, batch, tokens, heads)
-    _call(lib.mx_cache_attention, "mx_cache_attention", cache.device, cache._desc, q.data_ptr(),
-          _strides(q), batch, tokens, heads, *at, None if tree is None else tree.data_ptr(),
-          float(dim ** -0.5 if scale is None else scale), out.data_ptr(), _strides(out),
-          None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-          _stream(stream, cache.device))
+    _call(lib.mx_cache_attention, "mx_cache_attention", cache.device, stream, cache._desc,
+          q.data_ptr(), q_strides, batch, tokens, heads, *at, None if tree is None else tree.data_ptr(),
+          float(dim ** -0.5 if scale is None else scale), out.data_ptr(), out_strides,
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out if lse is None else (out, lse)
 
 

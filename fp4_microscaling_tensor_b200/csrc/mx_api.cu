@@ -93,14 +93,17 @@ mx_status check_batch(int64_t batch, int64_t tokens, const int32_t* table, int64
   return MX_OK;
 }
 
-// An outside tensor: its address and its three strides (elements of `size` bytes).
-mx_status check_rows(const void* p, const int64_t* strides, int size, mxk::Rows* out) {
+// An outside tensor: its address and its three strides (elements of `size` bytes).  The stride of a
+// dimension with one entry is never stepped over and may be anything.
+mx_status check_rows(const void* p, const int64_t* strides, int size, int64_t batch, int64_t tokens,
+                     int64_t heads, mxk::Rows* out) {
   if (!p || !strides) return MX_ERR_INVALID_ARG;
+  const int64_t dims[3] = {batch, tokens, heads};
   for (int i = 0; i < 3; ++i)
-    if (strides[i] < 0) return MX_ERR_INVALID_ARG;
+    if (dims[i] > 1 && strides[i] < 0) return MX_ERR_INVALID_ARG;
   if (!aligned16(p)) return MX_ERR_MISALIGNED;
   for (int i = 0; i < 3; ++i)
-    if ((strides[i] * size) % 16 != 0) return MX_ERR_MISALIGNED;
+    if (dims[i] > 1 && (strides[i] * size) % 16 != 0) return MX_ERR_MISALIGNED;
   *out = {const_cast<void*>(p), strides[0], strides[1], strides[2]};
   return MX_OK;
 }
@@ -542,8 +545,8 @@ mx_status mx_cache_append(const mx_cache_t* cache, const void* k, const void* v,
   if (st != MX_OK || batch == 0 || tokens == 0) return st;
   mxk::Rows rk, rv;
   const int size = xt == MX_BF16 ? 2 : 4;
-  if ((st = check_rows(k, k_strides, size, &rk)) != MX_OK) return st;
-  if ((st = check_rows(v, v_strides, size, &rv)) != MX_OK) return st;
+  if ((st = check_rows(k, k_strides, size, batch, tokens, c.kv_heads, &rk)) != MX_OK) return st;
+  if ((st = check_rows(v, v_strides, size, batch, tokens, c.kv_heads, &rv)) != MX_OK) return st;
   if (injected_failure()) return MX_ERR_CUDA;
   int n = 0;
   const cudaError_t e =
@@ -565,8 +568,8 @@ mx_status mx_cache_read(const mx_cache_t* cache, const int32_t* table, int64_t t
   if (st != MX_OK || batch == 0 || tokens == 0) return st;
   mxk::Rows rk, rv;
   const int size = yt == MX_BF16 ? 2 : 4;
-  if ((st = check_rows(k, k_strides, size, &rk)) != MX_OK) return st;
-  if ((st = check_rows(v, v_strides, size, &rv)) != MX_OK) return st;
+  if ((st = check_rows(k, k_strides, size, batch, tokens, c.kv_heads, &rk)) != MX_OK) return st;
+  if ((st = check_rows(v, v_strides, size, batch, tokens, c.kv_heads, &rv)) != MX_OK) return st;
   if (injected_failure()) return MX_ERR_CUDA;
   int n = 0;
   const cudaError_t e =
@@ -602,8 +605,8 @@ mx_status mx_cache_attention(const mx_cache_t* cache, const void* q, const int64
       max_pages * cache->page_size > (int64_t(1) << 30))
     return MX_ERR_UNSUPPORTED;
   if (batch == 0 || tokens == 0) return MX_OK;
-  if ((st = check_rows(q, q_strides, 2, &a.q)) != MX_OK) return st;
-  if ((st = check_rows(out, out_strides, 2, &a.out)) != MX_OK) return st;
+  if ((st = check_rows(q, q_strides, 2, batch, tokens, heads, &a.q)) != MX_OK) return st;
+  if ((st = check_rows(out, out_strides, 2, batch, tokens, heads, &a.out)) != MX_OK) return st;
   if (!workspace ||
       ws_bytes < mx_cache_attention_workspace_size(batch, tokens, heads, a.c.kv_heads,
                                                    a.c.head_dim))

@@ -42,6 +42,8 @@ __device__ __forceinline__ int perm(int i) { return i ^ ((i >> 1) & 1); }
 constexpr int kWarps = 4;
 constexpr int kStreamThreads = 32 * kWarps;
 
+constexpr float kSlack = 8.0f;
+
 template <int D, int NT>
 struct Geometry {
   // positions per tile: fewer where the accumulators leave few registers for the scores
@@ -67,6 +69,9 @@ constexpr int stream_smem() {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -144,11 +149,15 @@ struct Stream {
   const int lane, g, t4;
   const uint32_t ring;                            // shared address of the warp's ring
   const int log_sb;                               // log2 of the scale bytes of a position
+  // this lane's places in a tile: where its copies of keys and values go, its part of the keys of
+  // MMA row g, of the values of MMA columns 2 t4 and 2 t4 + 1, and their scales
+  uint32_t put_k, put_v, get_k[2], get_v[2], get_ks[2], get_vs[2];
 
   uint32_t q[NT][KS][2];                          // B operand of q K^T (f16 pairs)
   float mult[NT][2];                              // log2 weight per unit of raw score, this lane's
                                                   // two columns (query rows 8 nt + 2 t4, + 1)
-  float m[NT][2], l[NT][2];                       // running maximum (raw scores), partial sum
+  float m[NT][2], l[NT][2];                       // maximum in use (raw scores), partial sum
+  float mu[NT][2], lim[NT][2];                    // m in log2, and the score that moves it
   float o[NT][MT][4];
 
   // segment
@@ -161,7 +170,39 @@ struct Stream {
 
   __device__ __forceinline__ Stream(const AttnArgs& args, uint32_t ring_addr)
       : a(args), lane(threadIdx.x & 31), g(lane >> 2), t4(lane & 3), ring(ring_addr),
-        log_sb(log2_of(D) - args.c.log_block), seq(args, 0) {}
+        log_sb(N16 ? log2_of(D / 16) : log2_of(D) - args.c.log_block), seq(args, 0) {
+    constexpr int CH = D / 32;
+    const int i = lane / CH, piece = lane % CH, log_block = log2_of(D) - log_sb;
+    // Swizzles (of 16-byte pieces by position) that keep the loads below free of bank conflicts
+    if constexpr (D == 64) {
+      put_k = 32 * i + 16 * piece;
+      put_v = 32 * (i ^ ((i >> 2) & 1)) + 16 * piece;
+    } else if constexpr (D == 128) {
+      put_k = 64 * i + 16 * piece;
+      put_v = 64 * i + 16 * (piece ^ ((i >> 1) & 3));
+    } else {
+      put_k = 128 * i + 16 * (piece ^ ((i & 1) << 2));
+      put_v = 128 * i + 16 * (piece ^ (((i >> 1) & 3) << 1));
+    }
+    put_v += G::kCodes;
+    const int k = perm(g);
+#pragma unroll
+    for (int run = 0; run < 2; ++run) {  // runs of 32 (D = 64: 16) codes; D <= 128 has one
+      get_k[run] = D == 256 ? k * G::kRow + 16 * ((t4 + 4 * run) ^ ((k & 1) << 2))
+                            : k * G::kRow + t4 * KB;
+      const int d = D == 256 ? 128 * run + 32 * t4 : (D / 4) * t4;
+      get_ks[run] = 2 * G::kCodes + (k << log_sb) + (d >> log_block);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int v = perm(2 * t4 + e);
+      if constexpr (D == 64) get_v[e] = 32 * (v ^ ((v >> 2) & 1)) + 4 * g;
+      else if constexpr (D == 128) get_v[e] = 64 * v + 16 * ((g >> 1) ^ ((v >> 1) & 3)) + 8 * (g & 1);
+      else get_v[e] = 128 * v + 16 * (g ^ (((v >> 1) & 3) << 1));
+      get_v[e] += G::kCodes;
+      get_vs[e] = 2 * G::kCodes + G::kScales + (v << log_sb) + ((g * (D / 8)) >> log_block);
+    }
+  }
 
   // Query rows row0 .. row0 + 8 NT - 1 of the segment: f16, each row scaled by the power of two that
   // brings its largest magnitude to [2^14, 2^15) (exact for all values within 2^-28 of it; what is
@@ -217,7 +258,8 @@ struct Stream {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = 0.0f;
+      for (int e = 0; e < 2; ++e)
+        m[nt][e] = lim[nt][e] = -INFINITY, l[nt][e] = mu[nt][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -225,64 +267,65 @@ struct Stream {
     }
   }
 
-  // Lane i < tile / 16 gets the row of the cache (in units of slots of one head) where the tile's
-  // 16 positions from p + 16 i on begin, or -1.  (Pages are whole multiples of 16 slots.)
-  __device__ __forceinline__ int64_t page_rows(int p, int groups) const {
-    const int64_t pos = (int64_t)p + 16 * lane;
-    int64_t row = -1;
+  // Lane i < groups gets the place of the tile's 16 positions from p + 16 i on: the row of the cache
+  // (slots of one head) divided by 16, or -1.  (Pages are whole multiples of 16 slots.)
+  __device__ __forceinline__ int page_rows(int p, int groups) const {
+    const int pos = p + 16 * lane;
+    int row = -1;
     if (lane < groups && pos < end) {
-      row = a.table.slot(a.c, b, pos);
-      if (row >= 0) row += (int64_t)h << a.c.page_shift;
+      const int64_t slot = a.table.slot(a.c, b, pos);
+      if (slot >= 0) row = (int)((slot + ((int64_t)h << a.c.page_shift)) >> 4);
     }
     return row;
   }
 
   // Issues the copies of the TS positions from p on into slot `stage` of the ring.
   template <int TS>
-  __device__ __forceinline__ void issue(int p, int64_t rows, int stage) {
+  __device__ __forceinline__ void issue(int p, int rows, int stage) {
     constexpr int CH = D / 32;          // 16-byte pieces of a position's codes
-    constexpr int IT = TS * D / 1024;   // pieces per lane
+    constexpr int PER = 16 * CH / 32;   // pieces per lane of 16 positions
+    constexpr int T = TS / 16;
     const uint32_t st = ring + stage * G::kStage;
-    const int piece = lane % CH;
+    const bool full = p + TS <= end && __all_sync(0xffffffffu, lane >= T || rows >= 0);
+    const int i0 = lane / CH, piece = lane % CH;  // position (of 16) and piece of its first copy
 #pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int i = (32 / CH) * k + lane / CH;  // position in the tile
-      const int64_t row = __shfl_sync(0xffffffffu, rows, (32 / CH) * k / 16);
-      const bool ok = row >= 0 && p + i < end;
-      const int64_t at = ok ? (row + (i & 15)) * G::kRow + 16 * piece : 0;
-      uint32_t kd, vd;
-      if constexpr (D == 64) {
-        kd = 32 * i + 16 * piece;
-        vd = 32 * (i ^ ((i >> 2) & 1)) + 16 * piece;
-      } else if constexpr (D == 128) {
-        kd = 64 * i + 16 * piece;
-        vd = 64 * i + 16 * (piece ^ ((i >> 1) & 3));
-      } else {
-        kd = 128 * i + 16 * (piece ^ ((i & 1) << 2));
-        vd = 128 * i + 16 * (piece ^ (((i >> 1) & 3) << 1));
+    for (int gr = 0; gr < T; ++gr) {
+      const int row = __shfl_sync(0xffffffffu, rows, gr);
+      const int64_t at = (int64_t)row * (16 * G::kRow) + i0 * G::kRow + 16 * piece;
+      const uint8_t *ks = a.c.codes[0] + at, *vs = a.c.codes[1] + at;
+      const uint32_t kd = st + put_k + gr * 16 * G::kRow, vd = st + put_v + gr * 16 * G::kRow;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        // (head_dim 256: the swizzle of every other four positions differs in bit 6)
+        const uint32_t v = (D == 256 && (k & 1) ? vd ^ 64u : vd) + 512 * k;
+        if (full) {
+          cp_async16(kd + 512 * k, ks + 512 * k);
+          cp_async16(v, vs + 512 * k);
+        } else {
+          const bool ok = row >= 0 && p + 16 * gr + i0 + k * (32 / CH) < end;
+          cp_async16(kd + 512 * k, ok ? ks + 512 * k : a.c.codes[0], ok ? 16 : 0);
+          cp_async16(v, ok ? vs + 512 * k : a.c.codes[1], ok ? 16 : 0);
+        }
       }
-      cp_async16(st + kd, a.c.codes[0] + at, ok ? 16 : 0);
-      cp_async16(st + G::kCodes + vd, a.c.codes[1] + at, ok ? 16 : 0);
     }
     // scales: 16 positions hold 16 << log_sb contiguous bytes; a piece covers 16 >> log_sb positions
     const int i = (lane >> log_sb) * 16 + ((lane & ((1 << log_sb) - 1)) << (4 - log_sb));
-    const int64_t row = __shfl_sync(0xffffffffu, rows, (lane >> log_sb) & 3);
-    if (lane < (TS / 16 << log_sb)) {
+    const int row = __shfl_sync(0xffffffffu, rows, (lane >> log_sb) & 3);
+    if (lane < (T << log_sb)) {
       const int n = row >= 0 ? min(max(end - (p + i), 0), 16 >> log_sb) << log_sb : 0;
-      const int64_t at = n ? (row + (i & 15)) << log_sb : 0;
-      cp_async16(st + 2 * G::kCodes + (i << log_sb), a.c.scales[0] + at, n);
-      cp_async16(st + 2 * G::kCodes + G::kScales + (i << log_sb), a.c.scales[1] + at, n);
+      const int64_t at = n ? ((int64_t)row * 16 + (i & 15)) << log_sb : 0;
+      const uint32_t dst = st + 2 * G::kCodes + (i << log_sb);
+      cp_async16(dst, a.c.scales[0] + at, n);
+      cp_async16(dst + G::kScales, a.c.scales[1] + at, n);
     }
     cp_commit();
   }
 
-  // The TS positions from p on, in slot `stage`; rows: their page_rows.
+  // The TS positions from p on, the first of them at st in the ring; have: bit i says whether
+  // positions 16 i .. of them have a page.
   template <int TS>
-  __device__ __forceinline__ void compute(int p, int64_t rows, int stage) {
+  __device__ __forceinline__ void compute(int p, uint32_t have, uint32_t st, uint32_t st_scales) {
     constexpr int T = TS / 16;
-    const uint32_t kc = ring + stage * G::kStage, vc = kc + G::kCodes, ks = vc + G::kCodes,
-                   vs = ks + G::kScales;
-    const int log_block = a.c.log_block;
     float s[NT][T][4];
     // ---- scores
 #pragma unroll
@@ -291,26 +334,24 @@ struct Stream {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nt][mt][e] = 0.0f;
-      const int ia = 16 * mt + perm(g);  // and ia + 8
-      constexpr int RUNS = D == 256 ? 2 : 1;       // runs of 32 (D = 64: 16) codes
+      constexpr int RUNS = D == 256 ? 2 : 1;
       constexpr int RB = KB / RUNS;                // bytes of a run
+      constexpr bool kTwo = N16 && RB == 16;       // two scales in a run
 #pragma unroll
       for (int run = 0; run < RUNS; ++run) {
         uint32_t c[2][RB / 4], sc[2][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = ia + 8 * e;
-          const uint32_t piece = D == 256 ? (uint32_t)((t4 + 4 * run) ^ ((i & 1) << 2)) : (uint32_t)t4;
-          lds<RB>(kc + i * G::kRow + piece * RB, c[e]);
-          const uint32_t d0 = D == 256 ? 128 * run + 32 * t4 : (D / 4) * t4;
-          const uint32_t sa = ks + (i << log_sb) + (d0 >> log_block);
-          if constexpr (N16 && RB == 16) {  // two scales: 16 codes each
+          const int i = 16 * mt + 8 * e;           // and perm(g)
+          lds<RB>(st + get_k[run] + i * G::kRow, c[e]);
+          const uint32_t sa = st_scales + get_ks[run] + (i << log_sb);
+          if constexpr (kTwo) {
             const uint32_t f = scales_f16x2<FMT>(lds_u16(sa));
             sc[e][0] = __byte_perm(f, f, 0x1010);
             sc[e][1] = __byte_perm(f, f, 0x3232);
           } else {
             const uint32_t w = lds_u8(sa);
-            sc[e][0] = sc[e][1] = scales_f16x2<FMT>(w | (w << 8));
+            sc[e][0] = sc[e][1] = scales_f16x2<FMT>(w * 0x101u);
           }
         }
 #pragma unroll
@@ -320,8 +361,8 @@ struct Stream {
           e2m1x8_to_f16(c[1][wd], hb);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            ha[i] = mul_f16x2(ha[i], sc[0][(N16 && RB == 16) ? wd >> 1 : 0]);
-            hb[i] = mul_f16x2(hb[i], sc[1][(N16 && RB == 16) ? wd >> 1 : 0]);
+            ha[i] = mul_f16x2(ha[i], sc[0][kTwo ? wd >> 1 : 0]);
+            hb[i] = mul_f16x2(hb[i], sc[1][kTwo ? wd >> 1 : 0]);
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -334,7 +375,6 @@ struct Stream {
       }
     }
     // ---- masks: only tiles with new tokens, the end, or positions without a page
-    const uint32_t have = __ballot_sync(0xffffffffu, rows >= 0);
     if (p + TS > min(end, seq.base + 1) || (have & ((1u << T) - 1)) != (1u << T) - 1) {
 #pragma unroll
       for (int mt = 0; mt < T; ++mt)
@@ -350,46 +390,47 @@ struct Stream {
                 s[nt][mt][2 * half + e] = -INFINITY;
         }
     }
-    // ---- running maximum and weights
+    // ---- weights, relative to a maximum that follows the scores with a delay: it moves only when a
+    // score exceeds it by kSlack (in log2), so a weight may be up to 2^kSlack, and most tiles need no
+    // exchange between lanes and leave the outputs as they are
     uint32_t pb[NT][T][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mu[2];
+      float mx[2];
       bool grew = false;
-      float alpha[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(s[nt][0][e], s[nt][0][2 + e]);
+        mx[e] = fmaxf(s[nt][0][e], s[nt][0][2 + e]);
 #pragma unroll
-        for (int mt = 1; mt < T; ++mt) mx = fmaxf(mx, fmaxf(s[nt][mt][e], s[nt][mt][2 + e]));
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = fmaxf(m[nt][e], mx);
-        grew |= mn > m[nt][e];
-        mu[e] = mn == -INFINITY ? 0.0f : mn * mult[nt][e];
-        alpha[e] = m[nt][e] == -INFINITY ? 0.0f : ex2((m[nt][e] - mn) * mult[nt][e]);
-        m[nt][e] = mn;
+        for (int mt = 1; mt < T; ++mt) mx[e] = fmaxf(mx[e], fmaxf(s[nt][mt][e], s[nt][mt][2 + e]));
+        grew |= mx[e] > lim[nt][e];
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (m[nt][e] == -INFINITY) alpha[e] = 1.0f;  // nothing seen yet: nothing to scale
-          l[nt][e] *= alpha[e];
+          float mn = fmaxf(mx[e], m[nt][e]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+          // (no score yet: nothing to scale)
+          const float alpha = m[nt][e] == -INFINITY ? (mn == -INFINITY ? 1.0f : 0.0f)
+                                                    : ex2((m[nt][e] - mn) * mult[nt][e]);
+          m[nt][e] = mn;
+          mu[nt][e] = mn == -INFINITY ? 0.0f : mn * mult[nt][e];
+          lim[nt][e] = mn == -INFINITY ? mn : mn + kSlack / mult[nt][e];
+          l[nt][e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) o[nt][i][e] *= alpha, o[nt][i][2 + e] *= alpha;
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] *= alpha[e & 1];
       }
 #pragma unroll
       for (int mt = 0; mt < T; ++mt) {
         float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          w[e] = ex2(fmaf(s[nt][mt][e], mult[nt][e & 1], -mu[e & 1]));
+          w[e] = ex2(fmaf(s[nt][mt][e], mult[nt][e & 1], -mu[nt][e & 1]));
           l[nt][e & 1] += w[e];
         }
-        // binary16 weights, at most 1: 2^-11 each, and 2^-25 below the normal range
+        // binary16 weights: 2^-11 each, and 2^-25 below the normal range
         pb[nt][mt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
         pb[nt][mt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
       }
@@ -402,13 +443,9 @@ struct Stream {
       uint32_t sw[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = 16 * kt + 8 * (e >> 1) + perm(2 * t4 + (e & 1));
-        uint32_t at;
-        if constexpr (D == 64) at = 32 * (i ^ ((i >> 2) & 1)) + 4 * g;
-        else if constexpr (D == 128) at = 64 * i + 16 * ((g >> 1) ^ ((i >> 1) & 3)) + 8 * (g & 1);
-        else at = 128 * i + 16 * (g ^ (((i >> 1) & 3) << 1));
-        lds<VB>(vc + at, c[e]);
-        const uint32_t sa = vs + (i << log_sb) + ((uint32_t)(g * (D / 8)) >> log_block);
+        const int i = 16 * kt + 8 * (e >> 1);      // and perm(2 t4 + (e & 1))
+        lds<VB>(st + get_v[e & 1] + i * G::kRow, c[e]);
+        const uint32_t sa = st_scales + get_vs[e & 1] + (i << log_sb);
         sw[e] = (N16 && D == 256) ? lds_u16(sa) : lds_u8(sa);
       }
 #pragma unroll
@@ -447,34 +484,40 @@ struct Stream {
   template <int TS>
   __device__ __forceinline__ void run(int p0, int first, int step) {
     constexpr int S = G::kStages;
+    constexpr int PART = TS < 32 ? TS : 32;  // computed at a time (all of a tile at once outgrows the
+                                             // instruction cache)
     const int tiles = (end - p0 + TS - 1) / TS;
-    int64_t rows[S];  // page rows of the tiles in the ring
-#pragma unroll
-    for (int s = 0; s < S; ++s) rows[s] = -1;
-    int64_t ahead = page_rows(p0 + first * TS, TS / 16);
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-      const int i = first + s * step;
-      rows[s] = ahead;
-      if (i < tiles) issue<TS>(p0 + i * TS, ahead, s);
-      else cp_commit();
-      ahead = i + step < tiles ? page_rows(p0 + (i + step) * TS, TS / 16) : -1;
-    }
-    for (int base = first; base < tiles; base += S * step) {
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const int i = base + s * step;
-        if (i >= tiles) break;
-        const int next = i + (S - 1) * step;
-        rows[(s + S - 1) % S] = ahead;
-        if (next < tiles) issue<TS>(p0 + next * TS, ahead, (s + S - 1) % S);
-        else cp_commit();
-        ahead = next + step < tiles ? page_rows(p0 + (next + step) * TS, TS / 16) : -1;
-        cp_wait<S - 1>();
-        __syncwarp();
-        compute<TS>(p0 + i * TS, rows[s], s);
-        __syncwarp();
+    // which 16-position groups of the tiles in the ring have a page: four bits a tile, the oldest
+    // lowest
+    uint32_t have = 0;
+    int ahead = page_rows(p0 + first * TS, TS / 16);
+    int next = first;  // tile to copy
+    auto copy = [&](int slot, int place) {
+      if (next < tiles) {
+        issue<TS>(p0 + next * TS, ahead, slot);
+        have |= (__ballot_sync(0xffffffffu, ahead >= 0) & 15u) << (4 * place);
+      } else {
+        cp_commit();
       }
+      next += step;
+      ahead = next < tiles ? page_rows(p0 + next * TS, TS / 16) : -1;
+    };
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) copy(s, s);
+    int slot = 0;
+#pragma unroll 1
+    for (int i = first; i < tiles; i += step) {
+      copy(slot == 0 ? S - 1 : slot - 1, S - 1);
+      cp_wait<S - 1>();
+      __syncwarp();
+      const uint32_t st = ring + slot * G::kStage;
+#pragma unroll 1
+      for (int part = 0; part < TS / PART; ++part)
+        compute<PART>(p0 + i * TS + PART * part, have >> (PART / 16 * part),
+                      st + part * PART * G::kRow, st + ((part * PART) << log_sb));
+      __syncwarp();
+      have >>= 4;
+      slot = slot == S - 1 ? 0 : slot + 1;
     }
     cp_wait<0>();
     __syncwarp();

@@ -336,7 +336,8 @@ MX_API mx_status mx_test_matmul_abandon_last(void);
  *   - Outside tensors are [batch, tokens, heads, head_dim] with strides of their own for the first
  *     three dimensions, {batch, token, head}, in elements (host array of 3, read during the call);
  *     the last dimension is contiguous.  Strides are >= 0 and whole multiples of 16 bytes
- *     (MX_ERR_MISALIGNED); outputs must not overlap themselves.
+ *     (MX_ERR_MISALIGNED), but anything for a dimension with one entry; outputs must not overlap
+ *     themselves.
  *   - Tokens of a sequence behind its count are neither read nor written: rows of padding keep what
  *     they hold.
  *   - A position that the table does not reach (p < 0 or p >= max_pages * page_size), or whose table

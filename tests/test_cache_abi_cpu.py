@@ -21,7 +21,7 @@ def cache(**over):
     return _lib.Cache(**f)
 
 
-S = _lib.Strides(1024, 256, 128)
+S = _lib.Strides(1024, 256, 128, 1)
 
 
 def append(c=None, k=A, v=A, xt=BF16, ks=S, vs=S, b=2, t=3, table=A, ts=8, w=8, start=A, count=None):
@@ -89,7 +89,7 @@ def test_batches_and_tables(call):
 
 
 def test_outside_tensors():
-    odd, neg = _lib.Strides(1024, 260, 128), _lib.Strides(1024, -256, 128)
+    odd, neg = _lib.Strides(1024, 260, 128, 1), _lib.Strides(1024, -256, 128, 1)
     for call, names in ((append, ("k", "v")), (read, ("k", "v")), (attend, ("q", "out"))):
         for name in names:
             st = {"k": "ks", "v": "vs", "q": "qs", "out": "os"}[name]
@@ -101,9 +101,11 @@ def test_outside_tensors():
     assert append(xt=3) == INV and read(yt=-1) == INV
     arm()
     assert stopped(append(xt=F32, ks=odd, vs=odd))  # 260 fp32 are
+    arm()
+    assert stopped(append(t=1, ks=odd, vs=neg))     # a dimension with one entry
     for call in (append, read):
         arm()
-        assert stopped(call(ks=_lib.Strides(0, 0, 0)) if call is append else call())
+        assert stopped(call(ks=_lib.Strides(0, 0, 0, 1)) if call is append else call())
 
 
 def test_attention_arguments():
