@@ -69,6 +69,8 @@ mx_status check_cache(const mx_cache_t* c, mxk::CacheArgs* out) {
       c->block > c->head_dim || c->page_size < 16 || c->page_size > 256 ||
       (c->page_size & (c->page_size - 1)) != 0)
     return MX_ERR_UNSUPPORTED;
+  // (rows of 16 slots are counted in 32 bits: enough for any memory)
+  if (c->pages * c->kv_heads >= ((int64_t(1) << 31) * 16) / c->page_size) return MX_ERR_UNSUPPORTED;
   if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return MX_ERR_INVALID_ARG;
   if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
       !aligned16(c->v_scales))

@@ -20,11 +20,11 @@
 //     become f16 pairs along the positions, the layout the A operand of V^T p needs.
 //   * scores come out with positions in rows; movmatrix turns a pair of 8 x 8 weights tiles into the
 //     B operand of V^T p.  Nothing but codes and scales goes through shared memory.
-//   * every warp works for itself: cp.async brings its next tile (64 positions, keys and values, 8 KB
-//     + scales for D = 128) into a ring of its own while it computes; 12 warps per SM keep about 100
+//   * every warp works for itself: cp.async brings its next tiles (32 positions, keys and values, 4 KB
+//     + scales for D = 128) into a ring of its own while it computes; 16 warps per SM keep about 140
 //     KB in flight.  Bytes behind the end of the sequence, or of no page, arrive as zeros (a zero
 //     scale makes what the codes say harmless).
-// The warps of a block take the tiles of its piece in turn and join their results in shared memory at
+// The warps of a block share its piece's positions evenly and join their results in shared memory at
 // the piece's end.
 #include <math.h>
 
@@ -44,18 +44,23 @@ constexpr int kStreamThreads = 32 * kWarps;
 
 constexpr float kSlack = 8.0f;
 
+#ifndef MX_AT_BLOCKS
+#define MX_AT_BLOCKS 4
+#endif
+
+constexpr int kTile = 32;  // positions per tile
+
 template <int D, int NT>
 struct Geometry {
-  // positions per tile: fewer where the accumulators leave few registers for the scores
-  static constexpr int kTile = D == 256 || NT == 4 ? 32 : 64;
   static constexpr int kRow = D / 2;                       // code bytes of a position
   static constexpr int kCodes = kTile * kRow;              // bytes of a tile's key (value) codes
   static constexpr int kScales = kTile * (D / 16);         // most scale bytes of a tile's keys
   static constexpr int kStage = 2 * (kCodes + kScales);
-  static constexpr int kWarpBytes = 18432;                 // of shared memory
+  // blocks per SM: what the registers allow (D NT / 4 accumulators, D NT / 8 words of queries); the
+  // shared memory is split evenly
+  static constexpr int kBlocks = D * NT <= 128 ? MX_AT_BLOCKS : 2;
+  static constexpr int kWarpBytes = kBlocks == 4 ? 13824 : kBlocks == 3 ? 18432 : 27648;
   static constexpr int kStages = kWarpBytes / kStage;
-  // blocks per SM: registers for D NT / 4 accumulators and D NT / 8 words of queries
-  static constexpr int kBlocks = D * NT <= 128 ? 3 : 2;
   static constexpr int kJoinPitch = D + 4;                 // floats per row when warps join
 };
 
@@ -92,27 +97,33 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t* v) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint16_t v;
-  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u8 t, [%1];\n\tmov.b16 %0, t;\n\t}"
-               : "=h"(v) : "r"(addr));
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
       "%9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+      "%9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
 }
 
@@ -151,7 +162,8 @@ struct Stream {
   const int log_sb;                               // log2 of the scale bytes of a position
   // this lane's places in a tile: where its copies of keys and values go, its part of the keys of
   // MMA row g, of the values of MMA columns 2 t4 and 2 t4 + 1, and their scales
-  uint32_t put_k, put_v, get_k[2], get_v[2], get_ks[2], get_vs[2];
+  uint32_t put_k, put_v, put_s, get_k[2], get_v[2], get_ks[2], get_vs[2];
+  const uint8_t *src[2], *src_s[2];               // where its copies come from, in the cache's row 0
 
   uint32_t q[NT][KS][2];                          // B operand of q K^T (f16 pairs)
   float mult[NT][2];                              // log2 weight per unit of raw score, this lane's
@@ -163,7 +175,9 @@ struct Stream {
   // segment
   int64_t b;
   int h, group, row0;
-  int end;                                        // positions of the piece (exclusive)
+  int end;                                        // this warp's positions of the piece (exclusive)
+  int plain_end;                                  // up to here every row sees every position
+  bool holes;                                     // a position in between has no page
   Seq seq;
   int tok[NT][2];                                 // this lane's columns: token, and its tree word
   uint64_t word[NT][2];
@@ -185,6 +199,12 @@ struct Stream {
       put_v = 128 * i + 16 * (piece ^ (((i >> 1) & 3) << 1));
     }
     put_v += G::kCodes;
+    put_s = 2 * G::kCodes + 16 * lane;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      src[e] = args.c.codes[e] + i * G::kRow + 16 * piece;
+      src_s[e] = args.c.scales[e] + 16 * (lane & ((1 << log_sb) - 1));
+    }
     const int k = perm(g);
 #pragma unroll
     for (int run = 0; run < 2; ++run) {  // runs of 32 (D = 64: 16) codes; D <= 128 has one
@@ -267,73 +287,75 @@ struct Stream {
     }
   }
 
-  // Lane i < groups gets the place of the tile's 16 positions from p + 16 i on: the row of the cache
-  // (slots of one head) divided by 16, or -1.  (Pages are whole multiples of 16 slots.)
-  __device__ __forceinline__ int page_rows(int p, int groups) const {
+  // Lane i gets the place of the 16 positions from p + 16 i on: the row of the cache (slots of one
+  // head) divided by 16, or -1.  (Pages are whole multiples of 16 slots.)
+  __device__ __forceinline__ int page_rows(int p) const {
     const int pos = p + 16 * lane;
     int row = -1;
-    if (lane < groups && pos < end) {
+    if (pos < end) {
       const int64_t slot = a.table.slot(a.c, b, pos);
       if (slot >= 0) row = (int)((slot + ((int64_t)h << a.c.page_shift)) >> 4);
     }
     return row;
   }
 
-  // Issues the copies of the TS positions from p on into slot `stage` of the ring.
-  template <int TS>
-  __device__ __forceinline__ void issue(int p, int rows, int stage) {
-    constexpr int CH = D / 32;          // 16-byte pieces of a position's codes
-    constexpr int PER = 16 * CH / 32;   // pieces per lane of 16 positions
-    constexpr int T = TS / 16;
-    const uint32_t st = ring + stage * G::kStage;
-    const bool full = p + TS <= end && __all_sync(0xffffffffu, lane >= T || rows >= 0);
-    const int i0 = lane / CH, piece = lane % CH;  // position (of 16) and piece of its first copy
+  // Copies the tile from position p on to st in the ring; lanes from and from + 1 hold its page_rows.
+  // Bytes of positions behind the end, or without a page, arrive as zeros.
+  __device__ __forceinline__ void issue(int p, int rows, int from, uint32_t st) {
+    constexpr int PER = D / 64;         // 16-byte pieces per lane of 16 positions' codes
+    const int row0 = __shfl_sync(0xffffffffu, rows, from);
+    const int row1 = __shfl_sync(0xffffffffu, rows, from + 1);
+    const int sgr = lane >> log_sb;     // the 16 positions whose scales this lane copies
+    if (p + kTile <= end && (row0 | row1) >= 0) {
 #pragma unroll
-    for (int gr = 0; gr < T; ++gr) {
-      const int row = __shfl_sync(0xffffffffu, rows, gr);
-      const int64_t at = (int64_t)row * (16 * G::kRow) + i0 * G::kRow + 16 * piece;
-      const uint8_t *ks = a.c.codes[0] + at, *vs = a.c.codes[1] + at;
-      const uint32_t kd = st + put_k + gr * 16 * G::kRow, vd = st + put_v + gr * 16 * G::kRow;
+      for (int gr = 0; gr < 2; ++gr) {
+        const uint64_t at = (uint64_t)(uint32_t)(gr ? row1 : row0) * (16 * G::kRow);
+        const uint8_t *ks = src[0] + at, *vs = src[1] + at;
+        const uint32_t kd = st + put_k, vd = st + put_v;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        // (head_dim 256: the swizzle of every other four positions differs in bit 6)
-        const uint32_t v = (D == 256 && (k & 1) ? vd ^ 64u : vd) + 512 * k;
-        if (full) {
-          cp_async16(kd + 512 * k, ks + 512 * k);
-          cp_async16(v, vs + 512 * k);
-        } else {
-          const bool ok = row >= 0 && p + 16 * gr + i0 + k * (32 / CH) < end;
-          cp_async16(kd + 512 * k, ok ? ks + 512 * k : a.c.codes[0], ok ? 16 : 0);
-          cp_async16(v, ok ? vs + 512 * k : a.c.codes[1], ok ? 16 : 0);
+        for (int k = 0; k < PER; ++k) {
+          const int to = gr * 16 * G::kRow + 512 * k;
+          cp_async16(kd + to, ks + 512 * k);
+          cp_async16(((D == 256 && (k & 1)) ? vd ^ 64u : vd) + to, vs + 512 * k);
         }
       }
+      if (sgr < 2) {
+        const uint64_t at = (uint64_t)(uint32_t)(sgr ? row1 : row0) << (4 + log_sb);
+        cp_async16(st + put_s, src_s[0] + at);
+        cp_async16(st + put_s + G::kScales, src_s[1] + at);
+      }
+      return;
     }
-    // scales: 16 positions hold 16 << log_sb contiguous bytes; a piece covers 16 >> log_sb positions
-    const int i = (lane >> log_sb) * 16 + ((lane & ((1 << log_sb) - 1)) << (4 - log_sb));
-    const int row = __shfl_sync(0xffffffffu, rows, (lane >> log_sb) & 3);
-    if (lane < (T << log_sb)) {
-      const int n = row >= 0 ? min(max(end - (p + i), 0), 16 >> log_sb) << log_sb : 0;
-      const int64_t at = n ? ((int64_t)row * 16 + (i & 15)) << log_sb : 0;
-      const uint32_t dst = st + 2 * G::kCodes + (i << log_sb);
-      cp_async16(dst, a.c.scales[0] + at, n);
-      cp_async16(dst + G::kScales, a.c.scales[1] + at, n);
+#pragma unroll 1
+    for (int gr = 0; gr < 2; ++gr) {
+      const int row = gr ? row1 : row0, left = end - (p + 16 * gr);
+      if (row < 0 && left > 0) holes = true;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const bool ok = row >= 0 && lane / (D / 32) + k * (1024 / D) < left;
+        const uint64_t at = ok ? (uint64_t)row * (16 * G::kRow) + 512 * k : 0;
+        const int to = gr * 16 * G::kRow + 512 * k;
+        cp_async16(st + put_k + to, src[0] + at, ok ? 16 : 0);
+        cp_async16(st + ((D == 256 && (k & 1)) ? put_v ^ 64u : put_v) + to, src[1] + at, ok ? 16 : 0);
+      }
+      if (sgr == gr) {
+        // a piece of 16 bytes is the scales of 16 >> log_sb positions
+        const int first = (lane & ((1 << log_sb) - 1)) << (4 - log_sb);
+        const int n = row >= 0 ? min(max(left - first, 0), 16 >> log_sb) << log_sb : 0;
+        const uint64_t at = n ? (uint64_t)row << (4 + log_sb) : 0;
+        cp_async16(st + put_s, src_s[0] + at, n);
+        cp_async16(st + put_s + G::kScales, src_s[1] + at, n);
+      }
     }
-    cp_commit();
   }
 
-  // The TS positions from p on, the first of them at st in the ring; have: bit i says whether
-  // positions 16 i .. of them have a page.
-  template <int TS>
-  __device__ __forceinline__ void compute(int p, uint32_t have, uint32_t st, uint32_t st_scales) {
-    constexpr int T = TS / 16;
+  // The tile from position p on, at st in the ring.
+  __device__ __forceinline__ void compute(int p, uint32_t st) {
+    constexpr int T = kTile / 16;
     float s[NT][T][4];
     // ---- scores
 #pragma unroll
     for (int mt = 0; mt < T; ++mt) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][mt][e] = 0.0f;
       constexpr int RUNS = D == 256 ? 2 : 1;
       constexpr int RB = KB / RUNS;                // bytes of a run
       constexpr bool kTwo = N16 && RB == 16;       // two scales in a run
@@ -344,7 +366,7 @@ struct Stream {
         for (int e = 0; e < 2; ++e) {
           const int i = 16 * mt + 8 * e;           // and perm(g)
           lds<RB>(st + get_k[run] + i * G::kRow, c[e]);
-          const uint32_t sa = st_scales + get_ks[run] + (i << log_sb);
+          const uint32_t sa = st + get_ks[run] + (i << log_sb);
           if constexpr (kTwo) {
             const uint32_t f = scales_f16x2<FMT>(lds_u16(sa));
             sc[e][0] = __byte_perm(f, f, 0x1010);
@@ -369,19 +391,22 @@ struct Stream {
             const uint32_t f[4] = {ha[2 * e], hb[2 * e], ha[2 * e + 1], hb[2 * e + 1]};
             const int k = (RB / 2) * run + 2 * wd + e;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(s[nt][mt], f, q[nt][k][0], q[nt][k][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (k == 0) mma16816_zero(s[nt][mt], f, q[nt][k][0], q[nt][k][1]);
+              else mma16816(s[nt][mt], f, q[nt][k][0], q[nt][k][1]);
+            }
           }
         }
       }
     }
     // ---- masks: only tiles with new tokens, the end, or positions without a page
-    if (p + TS > min(end, seq.base + 1) || (have & ((1u << T) - 1)) != (1u << T) - 1) {
+    if (p + kTile > plain_end || holes) {
 #pragma unroll
       for (int mt = 0; mt < T; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int pos = p + 16 * mt + 8 * half + perm(g);
-          const bool in = pos < end && ((have >> mt) & 1);
+          const bool in = pos < end && (!holes || a.table.slot(a.c, b, pos) >= 0);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -445,7 +470,7 @@ struct Stream {
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * kt + 8 * (e >> 1);      // and perm(2 t4 + (e & 1))
         lds<VB>(st + get_v[e & 1] + i * G::kRow, c[e]);
-        const uint32_t sa = st_scales + get_vs[e & 1] + (i << log_sb);
+        const uint32_t sa = st + get_vs[e & 1] + (i << log_sb);
         sw[e] = (N16 && D == 256) ? lds_u16(sa) : lds_u8(sa);
       }
 #pragma unroll
@@ -480,44 +505,41 @@ struct Stream {
     }
   }
 
-  // The tiles first, first + step, ... of TS positions of [p0, end).
-  template <int TS>
-  __device__ __forceinline__ void run(int p0, int first, int step) {
+  // Positions [p0, end) (p0 a multiple of 16).
+  __device__ __forceinline__ void run(int p0) {
     constexpr int S = G::kStages;
-    constexpr int PART = TS < 32 ? TS : 32;  // computed at a time (all of a tile at once outgrows the
-                                             // instruction cache)
-    const int tiles = (end - p0 + TS - 1) / TS;
-    // which 16-position groups of the tiles in the ring have a page: four bits a tile, the oldest
-    // lowest
-    uint32_t have = 0;
-    int ahead = page_rows(p0 + first * TS, TS / 16);
-    int next = first;  // tile to copy
-    auto copy = [&](int slot, int place) {
-      if (next < tiles) {
-        issue<TS>(p0 + next * TS, ahead, slot);
-        have |= (__ballot_sync(0xffffffffu, ahead >= 0) & 15u) << (4 * place);
-      } else {
-        cp_commit();
+    if (p0 >= end) return;
+    holes = false;
+    plain_end = min(end, seq.base + 1);
+    // the places of the next 512 positions to copy, and of those behind them
+    int rows = page_rows(p0), rows_next = page_rows(p0 + 512);
+    int ahead = p0, from = 0;  // tile to copy, and its place in rows
+    uint32_t to = ring;        // where it goes
+    auto copy = [&]() {
+      if (ahead < end) {
+        issue(ahead, rows, from, to);
+        from += 2;
+        if (from == 32) {
+          from = 0;
+          rows = rows_next;
+          rows_next = page_rows(ahead + kTile + 512);
+        }
       }
-      next += step;
-      ahead = next < tiles ? page_rows(p0 + next * TS, TS / 16) : -1;
+      cp_commit();
+      ahead += kTile;
+      to = to == ring + (S - 1) * G::kStage ? ring : to + G::kStage;
     };
 #pragma unroll 1
-    for (int s = 0; s < S - 1; ++s) copy(s, s);
-    int slot = 0;
+    for (int s = 0; s < S - 1; ++s) copy();
+    uint32_t st = ring;
 #pragma unroll 1
-    for (int i = first; i < tiles; i += step) {
-      copy(slot == 0 ? S - 1 : slot - 1, S - 1);
+    for (int p = p0; p < end; p += kTile) {
+      copy();
       cp_wait<S - 1>();
       __syncwarp();
-      const uint32_t st = ring + slot * G::kStage;
-#pragma unroll 1
-      for (int part = 0; part < TS / PART; ++part)
-        compute<PART>(p0 + i * TS + PART * part, have >> (PART / 16 * part),
-                      st + part * PART * G::kRow, st + ((part * PART) << log_sb));
+      compute(p, st);
       __syncwarp();
-      have >>= 4;
-      slot = slot == S - 1 ? 0 : slot + 1;
+      st = st == ring + (S - 1) * G::kStage ? ring : st + G::kStage;
     }
     cp_wait<0>();
     __syncwarp();
@@ -535,7 +557,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   __shared__ int64_t s_scan[kWarps];
   __shared__ Share s_share;
   __shared__ float s_m[kWarps][R], s_l[kWarps][R];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
   griddep_wait();
   griddep_launch_next();
@@ -555,13 +577,12 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
       w.h = k.h;
       w.row0 = k.rt * R;
       w.seq = Seq(a, k.b);
-      const int p0 = k.c0 * kUnit;
-      w.end = min(k.end, k.c1 * kUnit);
+      // an equal run of 16-position groups for each warp
+      const int p0 = k.c0 * kUnit, groups = (min(k.end, k.c1 * kUnit) - p0 + 15) / 16;
+      w.end = min(min(k.end, k.c1 * kUnit), p0 + 16 * (groups * (warp + 1) / kWarps));
       w.load_queries();
       w.reset();
-      // long pieces: a tile per warp in turn; short ones: 16 positions per warp
-      if (w.end - p0 >= kWarps * G::kTile) w.template run<G::kTile>(p0, warp, kWarps);
-      else w.template run<16>(p0, warp, kWarps);
+      w.run(p0 + 16 * (groups * warp / kWarps));
 
       // join the warps: maxima first
 #pragma unroll
@@ -734,7 +755,7 @@ int row_tiles(int64_t rows, int dim) {
   return nt < most ? nt : most;
 }
 
-constexpr int kMaxStreamCtas = 3 * 160;  // thread blocks at most: 3 per SM
+constexpr int kMaxStreamCtas = 4 * 160;  // thread blocks at most: 4 per SM
 
 template <int D, int NT, int FMT, bool N16>
 cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches) {
