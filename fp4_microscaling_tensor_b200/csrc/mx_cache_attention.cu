@@ -20,8 +20,8 @@
 //     become f16 pairs along the positions, the layout the A operand of V^T p needs.
 //   * scores come out with positions in rows; movmatrix turns a pair of 8 x 8 weights tiles into the
 //     B operand of V^T p.  Nothing but codes and scales goes through shared memory.
-//   * every warp works for itself: cp.async brings its next tiles (32 positions, keys and values, 4 KB
-//     + scales for D = 128) into a ring of its own while it computes; 16 warps per SM keep about 140
+//   * every warp works for itself: cp.async brings its next tiles (64 positions, keys and values, 8 KB
+//     + scales for D = 128) into a ring of its own while it computes; 12 warps per SM keep about 100
 //     KB in flight.  Bytes behind the end of the sequence, or of no page, arrive as zeros (a zero
 //     scale makes what the codes say harmless).
 // The warps of a block share its piece's positions evenly and join their results in shared memory at
@@ -44,22 +44,20 @@ constexpr int kStreamThreads = 32 * kWarps;
 
 constexpr float kSlack = 8.0f;
 
-#ifndef MX_AT_BLOCKS
-#define MX_AT_BLOCKS 4
-#endif
 
-constexpr int kTile = 32;  // positions per tile
+constexpr int kPart = 32;  // positions computed at a time (more outgrow the instruction cache)
 
 template <int D, int NT>
 struct Geometry {
+  static constexpr int kTile = D == 256 ? 32 : 64;         // positions per tile of the ring
   static constexpr int kRow = D / 2;                       // code bytes of a position
   static constexpr int kCodes = kTile * kRow;              // bytes of a tile's key (value) codes
   static constexpr int kScales = kTile * (D / 16);         // most scale bytes of a tile's keys
   static constexpr int kStage = 2 * (kCodes + kScales);
   // blocks per SM: what the registers allow (D NT / 4 accumulators, D NT / 8 words of queries); the
   // shared memory is split evenly
-  static constexpr int kBlocks = D * NT <= 128 ? MX_AT_BLOCKS : 2;
-  static constexpr int kWarpBytes = kBlocks == 4 ? 13824 : kBlocks == 3 ? 18432 : 27648;
+  static constexpr int kBlocks = D * NT <= 128 ? 3 : 2;
+  static constexpr int kWarpBytes = kBlocks == 3 ? 18432 : 27648;
   static constexpr int kStages = kWarpBytes / kStage;
   static constexpr int kJoinPitch = D + 4;                 // floats per row when warps join
 };
@@ -127,22 +125,30 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   return d;
 }
 
-// Two scale codes (bytes 0 and 1 of w) -> f16 pair, times 2^-kScaleShift.  E4M3 by the hardware's
-// conversion.  UE5M3 has binary16's exponent: the code shifted to bits 7..14 is its value, except that
-// exponent 31 would be infinity.  Scaled by 2^-4 two ways -- a multiply, right below exponent 16 where
-// the shifted code loses its top exponent bit to the mask, and subtracting 4 from the exponent, right
-// from 5 on -- the larger one is the value: below 5 the second is negative or NaN, above 15 the first
-// is too small.
+// Scale codes -> f16, times 2^-kScaleShift: E4M3 by the hardware's conversion, UE5M3 (for which there
+// is none) by a table of all codes in shared memory.  pair: (x, y); both: x in both halves.
 template <int FMT>
-__device__ __forceinline__ uint32_t scales_f16x2(uint32_t w) {
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x, uint32_t y, uint32_t table) {
   uint32_t d;
   if constexpr (FMT == kE4M3) {
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(w));
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+        : "=r"(d) : "r"(__byte_perm(x, y, 0x0040)));
   } else {
-    const uint32_t x = __byte_perm(w, 0, 0x4140) << 7;
-    const uint32_t low = mul_f16x2(x & 0x3FFF3FFFu, 0x2C002C00u);
-    const uint32_t high = ((x | 0x80008000u) - 0x10001000u) ^ 0x80008000u;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(low), "r"(high));
+    uint32_t v[2];
+    lds<4>(table + 4 * x, &v[0]);
+    lds<4>(table + 4 * y, &v[1]);
+    d = __byte_perm(v[0], v[1], 0x5410);
+  }
+  return d;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_both(uint32_t x, uint32_t table) {
+  uint32_t d;
+  if constexpr (FMT == kE4M3) {
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+        : "=r"(d) : "r"(x * 0x101u));
+  } else {
+    lds<4>(table + 4 * x, &d);
   }
   return d;
 }
@@ -158,7 +164,7 @@ struct Stream {
 
   const AttnArgs& a;
   const int lane, g, t4;
-  const uint32_t ring;                            // shared address of the warp's ring
+  const uint32_t ring, table;                     // shared addresses: the warp's ring, the scales
   const int log_sb;                               // log2 of the scale bytes of a position
   // this lane's places in a tile: where its copies of keys and values go, its part of the keys of
   // MMA row g, of the values of MMA columns 2 t4 and 2 t4 + 1, and their scales
@@ -182,8 +188,9 @@ struct Stream {
   int tok[NT][2];                                 // this lane's columns: token, and its tree word
   uint64_t word[NT][2];
 
-  __device__ __forceinline__ Stream(const AttnArgs& args, uint32_t ring_addr)
+  __device__ __forceinline__ Stream(const AttnArgs& args, uint32_t ring_addr, uint32_t table_addr)
       : a(args), lane(threadIdx.x & 31), g(lane >> 2), t4(lane & 3), ring(ring_addr),
+        table(table_addr),
         log_sb(N16 ? log2_of(D / 16) : log2_of(D) - args.c.log_block), seq(args, 0) {
     constexpr int CH = D / 32;
     const int i = lane / CH, piece = lane % CH, log_block = log2_of(D) - log_sb;
@@ -299,17 +306,23 @@ struct Stream {
     return row;
   }
 
-  // Copies the tile from position p on to st in the ring; lanes from and from + 1 hold its page_rows.
+  // Copies the tile from position p on to st in the ring; lanes from on hold its page_rows.
   // Bytes of positions behind the end, or without a page, arrive as zeros.
   __device__ __forceinline__ void issue(int p, int rows, int from, uint32_t st) {
     constexpr int PER = D / 64;         // 16-byte pieces per lane of 16 positions' codes
-    const int row0 = __shfl_sync(0xffffffffu, rows, from);
-    const int row1 = __shfl_sync(0xffffffffu, rows, from + 1);
-    const int sgr = lane >> log_sb;     // the 16 positions whose scales this lane copies
-    if (p + kTile <= end && (row0 | row1) >= 0) {
+    constexpr int GR = G::kTile / 16;
+    int row[GR], all = 0;
 #pragma unroll
-      for (int gr = 0; gr < 2; ++gr) {
-        const uint64_t at = (uint64_t)(uint32_t)(gr ? row1 : row0) * (16 * G::kRow);
+    for (int gr = 0; gr < GR; ++gr) {
+      row[gr] = __shfl_sync(0xffffffffu, rows, from + gr);
+      all |= row[gr];
+    }
+    const int sgr = lane >> log_sb;     // the 16 positions whose scales this lane copies
+    const int srow = __shfl_sync(0xffffffffu, rows, from + (sgr & (GR - 1)));
+    if (p + G::kTile <= end && all >= 0) {
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr) {
+        const uint64_t at = (uint64_t)(uint32_t)row[gr] * (16 * G::kRow);
         const uint8_t *ks = src[0] + at, *vs = src[1] + at;
         const uint32_t kd = st + put_k, vd = st + put_v;
 #pragma unroll
@@ -319,21 +332,21 @@ struct Stream {
           cp_async16(((D == 256 && (k & 1)) ? vd ^ 64u : vd) + to, vs + 512 * k);
         }
       }
-      if (sgr < 2) {
-        const uint64_t at = (uint64_t)(uint32_t)(sgr ? row1 : row0) << (4 + log_sb);
+      if (sgr < GR) {
+        const uint64_t at = (uint64_t)(uint32_t)srow << (4 + log_sb);
         cp_async16(st + put_s, src_s[0] + at);
         cp_async16(st + put_s + G::kScales, src_s[1] + at);
       }
       return;
     }
 #pragma unroll 1
-    for (int gr = 0; gr < 2; ++gr) {
-      const int row = gr ? row1 : row0, left = end - (p + 16 * gr);
-      if (row < 0 && left > 0) holes = true;
+    for (int gr = 0; gr < GR; ++gr) {
+      const int r = __shfl_sync(0xffffffffu, rows, from + gr), left = end - (p + 16 * gr);
+      if (r < 0 && left > 0) holes = true;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const bool ok = row >= 0 && lane / (D / 32) + k * (1024 / D) < left;
-        const uint64_t at = ok ? (uint64_t)row * (16 * G::kRow) + 512 * k : 0;
+        const bool ok = r >= 0 && lane / (D / 32) + k * (1024 / D) < left;
+        const uint64_t at = ok ? (uint64_t)r * (16 * G::kRow) + 512 * k : 0;
         const int to = gr * 16 * G::kRow + 512 * k;
         cp_async16(st + put_k + to, src[0] + at, ok ? 16 : 0);
         cp_async16(st + ((D == 256 && (k & 1)) ? put_v ^ 64u : put_v) + to, src[1] + at, ok ? 16 : 0);
@@ -341,17 +354,17 @@ struct Stream {
       if (sgr == gr) {
         // a piece of 16 bytes is the scales of 16 >> log_sb positions
         const int first = (lane & ((1 << log_sb) - 1)) << (4 - log_sb);
-        const int n = row >= 0 ? min(max(left - first, 0), 16 >> log_sb) << log_sb : 0;
-        const uint64_t at = n ? (uint64_t)row << (4 + log_sb) : 0;
+        const int n = r >= 0 ? min(max(left - first, 0), 16 >> log_sb) << log_sb : 0;
+        const uint64_t at = n ? (uint64_t)r << (4 + log_sb) : 0;
         cp_async16(st + put_s, src_s[0] + at, n);
         cp_async16(st + put_s + G::kScales, src_s[1] + at, n);
       }
     }
   }
 
-  // The tile from position p on, at st in the ring.
-  __device__ __forceinline__ void compute(int p, uint32_t st) {
-    constexpr int T = kTile / 16;
+  // The kPart positions from p on, their codes at st and their scales at st_s (offset by the codes).
+  __device__ __forceinline__ void compute(int p, uint32_t st, uint32_t st_s) {
+    constexpr int T = kPart / 16;
     float s[NT][T][4];
     // ---- scores
 #pragma unroll
@@ -366,14 +379,19 @@ struct Stream {
         for (int e = 0; e < 2; ++e) {
           const int i = 16 * mt + 8 * e;           // and perm(g)
           lds<RB>(st + get_k[run] + i * G::kRow, c[e]);
-          const uint32_t sa = st + get_ks[run] + (i << log_sb);
+          const uint32_t sa = st_s + get_ks[run] + (i << log_sb);
           if constexpr (kTwo) {
-            const uint32_t f = scales_f16x2<FMT>(lds_u16(sa));
-            sc[e][0] = __byte_perm(f, f, 0x1010);
-            sc[e][1] = __byte_perm(f, f, 0x3232);
+            const uint32_t w = lds_u16(sa);
+            if constexpr (FMT == kE4M3) {
+              const uint32_t f = scale_pair<FMT>(w, w >> 8, table);
+              sc[e][0] = __byte_perm(f, f, 0x1010);
+              sc[e][1] = __byte_perm(f, f, 0x3232);
+            } else {
+              sc[e][0] = scale_both<FMT>(w & 0xFFu, table);
+              sc[e][1] = scale_both<FMT>(w >> 8, table);
+            }
           } else {
-            const uint32_t w = lds_u8(sa);
-            sc[e][0] = sc[e][1] = scales_f16x2<FMT>(w * 0x101u);
+            sc[e][0] = sc[e][1] = scale_both<FMT>(lds_u8(sa), table);
           }
         }
 #pragma unroll
@@ -400,7 +418,7 @@ struct Stream {
       }
     }
     // ---- masks: only tiles with new tokens, the end, or positions without a page
-    if (p + kTile > plain_end || holes) {
+    if (p + kPart > plain_end || holes) {
 #pragma unroll
       for (int mt = 0; mt < T; ++mt)
 #pragma unroll
@@ -470,15 +488,17 @@ struct Stream {
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * kt + 8 * (e >> 1);      // and perm(2 t4 + (e & 1))
         lds<VB>(st + get_v[e & 1] + i * G::kRow, c[e]);
-        const uint32_t sa = st + get_vs[e & 1] + (i << log_sb);
+        const uint32_t sa = st_s + get_vs[e & 1] + (i << log_sb);
         sw[e] = (N16 && D == 256) ? lds_u16(sa) : lds_u8(sa);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        sc[e][0] = scales_f16x2<FMT>(__byte_perm(sw[2 * e], sw[2 * e + 1], 0x0040));
-        sc[e][1] = (N16 && D == 256)
-                       ? scales_f16x2<FMT>(__byte_perm(sw[2 * e], sw[2 * e + 1], 0x0051))
-                       : sc[e][0];
+        if constexpr (N16 && D == 256) {  // two scales in a run
+          sc[e][0] = scale_pair<FMT>(sw[2 * e] & 0xFFu, sw[2 * e + 1] & 0xFFu, table);
+          sc[e][1] = scale_pair<FMT>(sw[2 * e] >> 8, sw[2 * e + 1] >> 8, table);
+        } else {
+          sc[e][0] = sc[e][1] = scale_pair<FMT>(sw[2 * e], sw[2 * e + 1], table);
+        }
       }
 #pragma unroll
       for (int wd = 0; wd < VB / 4; ++wd) {
@@ -505,10 +525,10 @@ struct Stream {
     }
   }
 
-  // Positions [p0, end) (p0 a multiple of 16).
+  // Positions [p0, end) (p0 a multiple of 16).  The queries are loaded while the first tiles are on
+  // their way.
   __device__ __forceinline__ void run(int p0) {
     constexpr int S = G::kStages;
-    if (p0 >= end) return;
     holes = false;
     plain_end = min(end, seq.base + 1);
     // the places of the next 512 positions to copy, and of those behind them
@@ -518,26 +538,30 @@ struct Stream {
     auto copy = [&]() {
       if (ahead < end) {
         issue(ahead, rows, from, to);
-        from += 2;
+        from += G::kTile / 16;
         if (from == 32) {
           from = 0;
           rows = rows_next;
-          rows_next = page_rows(ahead + kTile + 512);
+          rows_next = page_rows(ahead + G::kTile + 512);
         }
       }
       cp_commit();
-      ahead += kTile;
+      ahead += G::kTile;
       to = to == ring + (S - 1) * G::kStage ? ring : to + G::kStage;
     };
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) copy();
+    load_queries();
+    reset();
     uint32_t st = ring;
 #pragma unroll 1
-    for (int p = p0; p < end; p += kTile) {
+    for (int p = p0; p < end; p += G::kTile) {
       copy();
       cp_wait<S - 1>();
       __syncwarp();
-      compute(p, st);
+#pragma unroll 1
+      for (int part = 0; part < G::kTile && p + part < end; part += kPart)
+        compute(p + part, st + part * G::kRow, st + (part << log_sb));
       __syncwarp();
       st = st == ring + (S - 1) * G::kStage ? ring : st + G::kStage;
     }
@@ -557,6 +581,9 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   __shared__ int64_t s_scan[kWarps];
   __shared__ Share s_share;
   __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+  __shared__ uint32_t s_table[FMT == kUE5M3 ? 256 : 1];
+  if constexpr (FMT == kUE5M3)
+    for (int i = threadIdx.x; i < 256; i += kStreamThreads) s_table[i] = scale_f16x2<FMT>(i);
   const int warp = threadIdx.x >> 5;
   const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
   griddep_wait();
@@ -568,7 +595,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
 
   if (sh.lo < sh.hi) {
-    Stream<D, NT, FMT, N16> w(a, smem_addr(smem) + warp * G::kWarpBytes);
+    Stream<D, NT, FMT, N16> w(a, smem_addr(smem) + warp * G::kWarpBytes, smem_addr(s_table));
     w.group = group;
     Walk k;
     k.begin(a, group, R, sh);
@@ -580,8 +607,6 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
       // an equal run of 16-position groups for each warp
       const int p0 = k.c0 * kUnit, groups = (min(k.end, k.c1 * kUnit) - p0 + 15) / 16;
       w.end = min(min(k.end, k.c1 * kUnit), p0 + 16 * (groups * (warp + 1) / kWarps));
-      w.load_queries();
-      w.reset();
       w.run(p0 + 16 * (groups * warp / kWarps));
 
       // join the warps: maxima first
