@@ -1,7 +1,7 @@
 // mx_attention.cuh -- what the attention kernels over the FP4 cache share: how the work is cut, the
 // partial results of pieces, and small device helpers.
 //
-// The work of a call is a list of units: the 64-position chunks of every segment, a segment being
+// The work of a call is a list of units, the 64-position chunks of every segment, a segment being
 // (sequence, key/value head, tile of query rows).  The query rows of a key/value head are its
 // heads / kv_heads query heads of every token, row r = token r / G, head r % G.  How long the
 // sequences are is known on the device only, so every thread block adds the units up itself and
@@ -18,6 +18,10 @@ namespace mxk {
 namespace attn {
 
 constexpr int kUnit = 64;  // positions per unit
+
+#ifndef MX_AT_START
+#define MX_AT_START 4
+#endif
 
 // A sequence's numbers, cut to what is there: len positions, of which the newest `count` are this
 // call's tokens, from position base on (negative where the sequence is shorter than its count).
@@ -40,7 +44,13 @@ struct Seq {
   }
 };
 
-__device__ __forceinline__ int units_of(int end) { return max(1, (end + kUnit - 1) / kUnit); }
+// Starting a piece costs a block about as much time as kStart units (loading queries, filling its
+// pipeline, joining its warps), so every segment counts that many units more than it has, in front;
+// a share that would begin or end within them begins or ends at the segment instead.
+constexpr int kStart = MX_AT_START;
+__device__ __forceinline__ int units_of(int end) {
+  return kStart + max(1, (end + kUnit - 1) / kUnit);
+}
 
 // Units of one key/value head of sequence b.
 __device__ __forceinline__ int64_t head_units(const AttnArgs& a, int64_t b, int group, int rows) {
@@ -50,6 +60,12 @@ __device__ __forceinline__ int64_t head_units(const AttnArgs& a, int64_t b, int 
   int64_t n = 0;
   for (int rt = 0; rt < tiles; ++rt) n += units_of(s.end(a, group, rows, rt));
   return n;
+}
+
+// a / b for a >= 0, b > 0 (the 64-bit division is an order of magnitude slower).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 // Where a thread block's share of the list begins, and how long the list is.
@@ -86,7 +102,8 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, int group, int row
   }
   // (a list of 2^52 units, where the product would not fit, would take years)
   const int n = (int)min((int64_t)ctas, total);
-  const int64_t lo = cta < n ? total * cta / n : total, hi = cta < n ? total * (cta + 1) / n : total;
+  const int64_t lo = cta < n ? divide(total * cta, n) : total;
+  const int64_t hi = cta < n ? divide(total * (cta + 1), n) : total;
   const int64_t first = before + incl - sum;
   if (lo < hi && lo >= first && lo < first + sum) {
     int64_t at = lo - first, b = b0;
@@ -101,46 +118,51 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, int group, int row
   __syncthreads();
 }
 
-// The block that unit u belongs to (the inverse of find_share's split).
+// The block whose share unit u is in (the inverse of find_share's split).
 __device__ __forceinline__ int block_of(int64_t u, const Share& sh) {
-  return (int)(((u + 1) * sh.blocks - 1) / sh.total);
+  return (int)divide((u + 1) * sh.blocks - 1, sh.total);
 }
 
-// A walk over the pieces of a share.
+// A walk over the pieces of a share: segment (b, h, rt), its 64-position chunks c0 .. c1 - 1 of `n`.
 struct Walk {
   int64_t b;
-  int h, rt;           // segment
-  int c0, c1, n;       // its units of this share, and all of them
-  int end;             // positions the tile sees at most
+  int h, rt;
+  int c0, c1, n;
+  int end;             // positions the tile's rows see at most
   int64_t left;        // units of the share behind this piece
   int64_t u0;          // the list's place of the segment's first unit
-  __device__ __forceinline__ void set(const AttnArgs& a, int group, int rows, const Seq& s,
-                                      int first) {
+  __device__ __forceinline__ void set(const AttnArgs& a, int group, int rows, const Seq& s, int at) {
     end = s.end(a, group, rows, rt);
-    n = units_of(end);
-    c0 = first;
-    c1 = (int)min((int64_t)n, c0 + left);
-    left -= c1 - c0;
+    const int units = units_of(end);
+    const int take = (int)min((int64_t)(units - at), left);
+    n = units - kStart;
+    c0 = max(0, at - kStart);
+    c1 = at + take - kStart;
+    left -= take;
   }
-  __device__ __forceinline__ void begin(const AttnArgs& a, int group, int rows, const Share& sh) {
+  // The share's first piece; false if there is none.
+  __device__ __forceinline__ bool begin(const AttnArgs& a, int group, int rows, const Share& sh) {
+    if (sh.lo >= sh.hi) return false;
     b = sh.b;
     const Seq s(a, b);
     const int64_t per = head_units(a, b, group, rows);
-    h = (int)(sh.off / per);
+    h = (int)divide(sh.off, per);
     int64_t at = sh.off - h * per;
     rt = 0;
-    int m = units_of(s.end(a, group, rows, 0));
-    while (at >= m) {
+    for (int m = units_of(s.end(a, group, rows, 0)); at >= m;
+         m = units_of(s.end(a, group, rows, ++rt)))
       at -= m;
-      m = units_of(s.end(a, group, rows, ++rt));
-    }
-    left = sh.hi - sh.lo;
     u0 = sh.lo - at;
+    if (at <= kStart) at = 0;
+    left = sh.hi - (u0 + at);
+    if (left <= kStart && at == 0) return false;
     set(a, group, rows, s, (int)at);
+    return true;
   }
-  // The next piece; only when left > 0.
-  __device__ __forceinline__ void next(const AttnArgs& a, int group, int rows) {
-    u0 += n;
+  // The next piece; false if there is none.
+  __device__ __forceinline__ bool next(const AttnArgs& a, int group, int rows) {
+    if (left <= kStart) return false;
+    u0 += n + kStart;
     if (++rt >= Seq(a, b).tiles(group, rows)) {
       rt = 0;
       if (++h >= a.c.kv_heads) {
@@ -150,6 +172,7 @@ struct Walk {
       }
     }
     set(a, group, rows, Seq(a, b), 0);
+    return true;
   }
   __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == n; }
 };

@@ -59,15 +59,14 @@ struct Geometry {
   static constexpr int kBlocks = D * NT <= 128 ? 3 : 2;
   static constexpr int kWarpBytes = kBlocks == 3 ? 18432 : 27648;
   static constexpr int kStages = kWarpBytes / kStage;
-  static constexpr int kJoinPitch = D + 4;                 // floats per row when warps join
+  // When the warps join, each one's outputs take the last kJoin slots of its ring; the first kEarly
+  // are being filled for the next piece meanwhile.
+  static constexpr int kJoinPitch = D + 4;                 // floats per row
+  static constexpr int kJoin = (8 * NT * kJoinPitch * 4 + kStage - 1) / kStage;
+  static constexpr int kEarly = kJoin == 1 ? kStages - 1 : kStages - kJoin;
+  static constexpr int kJoinAt = (kStages - kJoin) * kStage;
+  static_assert(kEarly >= 1 && kEarly < kStages, "ring slots");
 };
-
-template <int D, int NT>
-constexpr int stream_smem() {
-  // rings, and behind them the scale table; the warps' results reuse their rings
-  static_assert(NT * 8 * Geometry<D, NT>::kJoinPitch * 4 <= Geometry<D, NT>::kWarpBytes, "join buffers");
-  return kWarps * Geometry<D, NT>::kWarpBytes;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -525,45 +524,62 @@ struct Stream {
     }
   }
 
-  // Positions [p0, end) (p0 a multiple of 16).  The queries are loaded while the first tiles are on
-  // their way.
-  __device__ __forceinline__ void run(int p0) {
-    constexpr int S = G::kStages;
+  // What the copies are at: the next position to copy, the places of the 512 positions around it and
+  // of those behind them, its place in `rows`, and where it goes.
+  int ahead, rows, rows_next, from;
+  uint32_t to;
+
+  __device__ __forceinline__ void copy() {
+    if (ahead < end) {
+      issue(ahead, rows, from, to);
+      from += G::kTile / 16;
+      if (from == 32) {
+        from = 0;
+        rows = rows_next;
+        rows_next = page_rows(ahead + G::kTile + 512);
+      }
+    }
+    cp_commit();
+    ahead += G::kTile;
+    to = to == ring + (G::kStages - 1) * G::kStage ? ring : to + G::kStage;
+  }
+
+  // A piece: this warp's positions [p0, p1) (p0 a multiple of 16) of segment (b_, h_, row0_ ..).
+  // Starts the first copies, and loads the queries while they are on their way.
+  __device__ __forceinline__ void begin(int64_t b_, int h_, int row0_, int p0, int p1) {
+    b = b_;
+    h = h_;
+    row0 = row0_;
+    seq = Seq(a, b);
+    end = p1;
     holes = false;
     plain_end = min(end, seq.base + 1);
-    // the places of the next 512 positions to copy, and of those behind them
-    int rows = page_rows(p0), rows_next = page_rows(p0 + 512);
-    int ahead = p0, from = 0;  // tile to copy, and its place in rows
-    uint32_t to = ring;        // where it goes
-    auto copy = [&]() {
-      if (ahead < end) {
-        issue(ahead, rows, from, to);
-        from += G::kTile / 16;
-        if (from == 32) {
-          from = 0;
-          rows = rows_next;
-          rows_next = page_rows(ahead + G::kTile + 512);
-        }
-      }
-      cp_commit();
-      ahead += G::kTile;
-      to = to == ring + (S - 1) * G::kStage ? ring : to + G::kStage;
-    };
+    ahead = p0;
+    rows = page_rows(p0);
+    rows_next = page_rows(p0 + 512);
+    from = 0;
+    to = ring;
 #pragma unroll 1
-    for (int s = 0; s < S - 1; ++s) copy();
+    for (int s = 0; s < G::kEarly; ++s) copy();
     load_queries();
+  }
+
+  // The rest of it.
+  __device__ __forceinline__ void run(int p0) {
     reset();
+#pragma unroll 1
+    for (int s = G::kEarly; s < G::kStages - 1; ++s) copy();
     uint32_t st = ring;
 #pragma unroll 1
     for (int p = p0; p < end; p += G::kTile) {
       copy();
-      cp_wait<S - 1>();
+      cp_wait<G::kStages - 1>();
       __syncwarp();
 #pragma unroll 1
       for (int part = 0; part < G::kTile && p + part < end; part += kPart)
         compute(p + part, st + part * G::kRow, st + (part << log_sb));
       __syncwarp();
-      st = st == ring + (S - 1) * G::kStage ? ring : st + G::kStage;
+      st = st == ring + (G::kStages - 1) * G::kStage ? ring : st + G::kStage;
     }
     cp_wait<0>();
     __syncwarp();
@@ -594,22 +610,22 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   Record mine{0, 0, 0, -1, 0};
   const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
 
-  if (sh.lo < sh.hi) {
+  Walk k;
+  if (k.begin(a, group, R, sh)) {
     Stream<D, NT, FMT, N16> w(a, smem_addr(smem) + warp * G::kWarpBytes, smem_addr(s_table));
     w.group = group;
-    Walk k;
-    k.begin(a, group, R, sh);
-    while (true) {
-      w.b = k.b;
-      w.h = k.h;
-      w.row0 = k.rt * R;
-      w.seq = Seq(a, k.b);
+    int p0;
+    auto begin = [&] {
       // an equal run of 16-position groups for each warp
-      const int p0 = k.c0 * kUnit, groups = (min(k.end, k.c1 * kUnit) - p0 + 15) / 16;
-      w.end = min(min(k.end, k.c1 * kUnit), p0 + 16 * (groups * (warp + 1) / kWarps));
-      w.run(p0 + 16 * (groups * warp / kWarps));
+      const int first = k.c0 * kUnit, last = min(k.end, k.c1 * kUnit), groups = (last - first + 15) / 16;
+      p0 = first + 16 * (groups * warp / kWarps);
+      w.begin(k.b, k.h, k.rt * R, p0, min(last, first + 16 * (groups * (warp + 1) / kWarps)));
+    };
+    begin();
+    while (true) {
+      w.run(p0);
 
-      // join the warps: maxima first
+      // this warp's maxima, sums and outputs
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -623,8 +639,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
             s_l[warp][r] = l;
           }
         }
-      // this warp's outputs into its own ring
-      float* mine_o = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
+      float* mine_o = reinterpret_cast<float*>(smem + warp * G::kWarpBytes + G::kJoinAt);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -634,11 +649,18 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
             *reinterpret_cast<float2*>(mine_o + (8 * nt + 2 * w.t4 + e) * G::kJoinPitch +
                                        (D / 8) * w.g + 2 * i) =
                 make_float2(w.o[nt][i][e], w.o[nt][i][2 + e]);
-      __syncthreads();
 
-      const int rows = min(R, w.seq.count * group - w.row0);
+      // the next piece's first copies before this one's join
+      const int64_t b = k.b;
+      const int h = k.h, row0 = k.rt * R, rows = min(R, w.seq.count * group - row0);
       const bool whole = k.whole();
       float* part = partial(a, ctas, R, D, 2 * cta + (k.c0 == 0));
+      if (k.c0 == 0 && !whole)
+        mine = {b, h, k.rt, block_of(k.u0 + k.n + kStart - 1, sh), 0};
+      const bool more = k.next(a, group, R);
+      if (more) begin();
+      __syncthreads();
+
       for (int i = threadIdx.x; i < R * (D / 8); i += kStreamThreads) {
         const int r = i / (D / 8), d = 8 * (i % (D / 8));
         if (r >= rows) break;
@@ -653,20 +675,21 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
         for (int x = 0; x < kWarps; ++x) {
           const float f = ex2(s_m[x][r] - mu);
           l += s_l[x][r] * f;
-          const float* src = reinterpret_cast<const float*>(smem + x * G::kWarpBytes) +
-                             r * G::kJoinPitch + d;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] += src[e] * f;
+          const float4* src = reinterpret_cast<const float4*>(
+              smem + x * G::kWarpBytes + G::kJoinAt + (r * G::kJoinPitch + d) * 4);
+          const float4 v0 = src[0], v1 = src[1];
+          y[0] += v0.x * f, y[1] += v0.y * f, y[2] += v0.z * f, y[3] += v0.w * f;
+          y[4] += v1.x * f, y[5] += v1.y * f, y[6] += v1.z * f, y[7] += v1.w * f;
         }
         if (whole) {
-          const int row = w.row0 + r, t = row / group, head = k.h * group + row % group;
+          const int row = row0 + r, t = row / group, head = h * group + row % group;
           const float f = l == 0.0f ? 0.0f : gv / l;
           const uint4 v = make_uint4(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f),
                                      pack_bf16x2(y[4] * f, y[5] * f), pack_bf16x2(y[6] * f, y[7] * f));
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out.p) +
-                                    row_offset(a.out, k.b, t, head) + d) = v;
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out.p) + row_offset(a.out, b, t, head) +
+                                    d) = v;
           if (a.lse && d == 0)
-            a.lse[(k.b * a.tokens + t) * a.heads + head] =
+            a.lse[(b * a.tokens + t) * a.heads + head] =
                 l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
         } else {
           float4* dst = reinterpret_cast<float4*>(part + 2 * R + r * D + d);
@@ -675,10 +698,8 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
           if (d == 0) part[r] = mx, part[R + r] = l;
         }
       }
-      if (k.c0 == 0 && !whole) mine = {k.b, k.h, k.rt, block_of(k.u0 + k.n - 1, sh), 0};
       __syncthreads();
-      if (k.left <= 0) break;
-      k.next(a, group, R);
+      if (!more) break;
     }
   }
   if (threadIdx.x == 0) *rec = mine;
@@ -785,7 +806,7 @@ constexpr int kMaxStreamCtas = 4 * 160;  // thread blocks at most: 4 per SM
 template <int D, int NT, int FMT, bool N16>
 cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches) {
   static std::atomic<bool> attr[kMaxDevices];
-  constexpr int smem = stream_smem<D, NT>();
+  constexpr int smem = kWarps * Geometry<D, NT>::kWarpBytes;
   auto* kern = k_attention_stream<D, NT, FMT, N16>;
   cudaError_t e = allow_dynamic_smem(attr, kern, smem);
   if (e != cudaSuccess) return e;
