@@ -669,8 +669,8 @@ def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, 
 
 
 def matmul_gave_up():
-    """Number of matmul thread blocks whose bounded waits ran out since the last call (0 normally);
-    synchronizes the device."""
+    """Number of matmul and attention thread blocks whose bounded waits ran out since the last call
+    (0 normally); synchronizes the device."""
     c = ctypes.c_uint(0)
     check(lib.mx_matmul_gave_up(ctypes.byref(c)), "mx_matmul_gave_up")
     return int(c.value)

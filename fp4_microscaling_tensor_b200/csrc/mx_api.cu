@@ -390,7 +390,11 @@ mx_status mx_matmul_prepare_scales(const uint8_t* scales, int64_t rows, int64_t 
 
 mx_status mx_matmul_gave_up(unsigned int* count) {
   if (!count) return MX_ERR_INVALID_ARG;
-  return from_cuda(mxk::matmul_gave_up(count));
+  unsigned int attention = 0;
+  cudaError_t e = mxk::matmul_gave_up(count);
+  if (e == cudaSuccess) e = mxk::attention_gave_up(&attention);
+  if (e == cudaSuccess) *count += attention;
+  return from_cuda(e);
 }
 
 mx_status mx_test_matmul_abandon_last(void) { return from_cuda(mxk::matmul_abandon_last()); }

@@ -11,17 +11,21 @@
 // and k_attention_join adds them up in the order of the list, so results do not depend on timing.
 #pragma once
 
+#include <math.h>
+
 #include "mx_cache.h"
 #include "mx_device.cuh"
 
 namespace mxk {
 namespace attn {
 
-constexpr int kUnit = 64;  // positions per unit
-
-#ifndef MX_AT_START
-#define MX_AT_START 4
-#endif
+// How a kernel cuts the work: query rows per tile, query heads per key/value head, positions per unit,
+// and what starting a piece costs a block (loading queries, filling its pipeline, joining), in units:
+// every segment counts that many units more than it has, in front; a share that would begin or end
+// within them begins or ends at the segment instead.
+struct Cut {
+  int rows, group, unit, start;
+};
 
 // A sequence's numbers, cut to what is there: len positions, of which the newest `count` are this
 // call's tokens, from position base on (negative where the sequence is shorter than its count).
@@ -34,31 +38,27 @@ struct Seq {
     base = len - count;
   }
   // Tiles of `rows` query rows, and the positions that the rows of tile rt see at most.
-  __device__ __forceinline__ int tiles(int group, int rows) const {
-    return (int)(((int64_t)count * group + rows - 1) / rows);
+  __device__ __forceinline__ int tiles(const Cut& c) const {
+    return (int)(((int64_t)count * c.group + c.rows - 1) / c.rows);
   }
-  __device__ __forceinline__ int end(const AttnArgs& a, int group, int rows, int rt) const {
+  __device__ __forceinline__ int end(const AttnArgs& a, const Cut& c, int rt) const {
     if (a.tree) return len;
-    const int64_t last = ((int64_t)(rt + 1) * rows - 1) / group;  // the tile's last token
+    const int64_t last = ((int64_t)(rt + 1) * c.rows - 1) / c.group;  // the tile's last token
     return max(0, (int)min((int64_t)len, base + min((int64_t)count - 1, last) + 1));
   }
 };
 
-// Starting a piece costs a block about as much time as kStart units (loading queries, filling its
-// pipeline, joining its warps), so every segment counts that many units more than it has, in front;
-// a share that would begin or end within them begins or ends at the segment instead.
-constexpr int kStart = MX_AT_START;
-__device__ __forceinline__ int units_of(int end) {
-  return kStart + max(1, (end + kUnit - 1) / kUnit);
+__device__ __forceinline__ int units_of(const Cut& c, int end) {
+  return c.start + max(1, (end + c.unit - 1) / c.unit);
 }
 
 // Units of one key/value head of sequence b.
-__device__ __forceinline__ int64_t head_units(const AttnArgs& a, int64_t b, int group, int rows) {
+__device__ __forceinline__ int64_t head_units(const AttnArgs& a, int64_t b, const Cut& c) {
   const Seq s(a, b);
-  const int tiles = s.tiles(group, rows);
-  if (a.tree || tiles <= 1) return tiles ? (int64_t)tiles * units_of(s.end(a, group, rows, 0)) : 0;
+  const int tiles = s.tiles(c);
+  if (a.tree || tiles <= 1) return tiles ? (int64_t)tiles * units_of(c, s.end(a, c, 0)) : 0;
   int64_t n = 0;
-  for (int rt = 0; rt < tiles; ++rt) n += units_of(s.end(a, group, rows, rt));
+  for (int rt = 0; rt < tiles; ++rt) n += units_of(c, s.end(a, c, rt));
   return n;
 }
 
@@ -79,13 +79,13 @@ struct Share {
 // All THREADS threads; scratch: THREADS / 32 values.  Each thread sums a run of sequences; the one
 // whose run holds the share's first unit walks it again.
 template <int THREADS>
-__device__ __forceinline__ void find_share(const AttnArgs& a, int group, int rows, int cta, int ctas,
+__device__ __forceinline__ void find_share(const AttnArgs& a, const Cut& c, int cta, int ctas,
                                            int64_t* scratch, Share* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t per = (a.batch + THREADS - 1) / THREADS;
   const int64_t b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   int64_t sum = 0;
-  for (int64_t b = b0; b < b1; ++b) sum += head_units(a, b, group, rows) * a.c.kv_heads;
+  for (int64_t b = b0; b < b1; ++b) sum += head_units(a, b, c) * a.c.kv_heads;
   int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -108,7 +108,7 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, int group, int row
   if (lo < hi && lo >= first && lo < first + sum) {
     int64_t at = lo - first, b = b0;
     for (; b < b1; ++b) {
-      const int64_t m = head_units(a, b, group, rows) * a.c.kv_heads;
+      const int64_t m = head_units(a, b, c) * a.c.kv_heads;
       if (at < m) break;
       at -= m;
     }
@@ -131,51 +131,59 @@ struct Walk {
   int end;             // positions the tile's rows see at most
   int64_t left;        // units of the share behind this piece
   int64_t u0;          // the list's place of the segment's first unit
-  __device__ __forceinline__ void set(const AttnArgs& a, int group, int rows, const Seq& s, int at) {
-    end = s.end(a, group, rows, rt);
-    const int units = units_of(end);
+  __device__ __forceinline__ void set(const AttnArgs& a, const Cut& c, const Seq& s, int at) {
+    end = s.end(a, c, rt);
+    const int units = units_of(c, end);
     const int take = (int)min((int64_t)(units - at), left);
-    n = units - kStart;
-    c0 = max(0, at - kStart);
-    c1 = at + take - kStart;
+    n = units - c.start;
+    c0 = max(0, at - c.start);
+    c1 = at + take - c.start;
     left -= take;
   }
   // The share's first piece; false if there is none.
-  __device__ __forceinline__ bool begin(const AttnArgs& a, int group, int rows, const Share& sh) {
+  __device__ __forceinline__ bool begin(const AttnArgs& a, const Cut& c, const Share& sh) {
     if (sh.lo >= sh.hi) return false;
     b = sh.b;
     const Seq s(a, b);
-    const int64_t per = head_units(a, b, group, rows);
+    const int64_t per = head_units(a, b, c);
     h = (int)divide(sh.off, per);
     int64_t at = sh.off - h * per;
     rt = 0;
-    for (int m = units_of(s.end(a, group, rows, 0)); at >= m;
-         m = units_of(s.end(a, group, rows, ++rt)))
+    for (int m = units_of(c, s.end(a, c, 0)); at >= m;
+         m = units_of(c, s.end(a, c, ++rt)))
       at -= m;
     u0 = sh.lo - at;
-    if (at <= kStart) at = 0;
+    if (at <= c.start) at = 0;
     left = sh.hi - (u0 + at);
-    if (left <= kStart && at == 0) return false;
-    set(a, group, rows, s, (int)at);
+    if (left <= c.start && at == 0) return false;
+    set(a, c, s, (int)at);
     return true;
   }
   // The next piece; false if there is none.
-  __device__ __forceinline__ bool next(const AttnArgs& a, int group, int rows) {
-    if (left <= kStart) return false;
-    u0 += n + kStart;
-    if (++rt >= Seq(a, b).tiles(group, rows)) {
+  __device__ __forceinline__ bool next(const AttnArgs& a, const Cut& c) {
+    if (left <= c.start) return false;
+    u0 += n + c.start;
+    if (++rt >= Seq(a, b).tiles(c)) {
       rt = 0;
       if (++h >= a.c.kv_heads) {
         h = 0;
         do ++b;
-        while (Seq(a, b).tiles(group, rows) == 0);
+        while (Seq(a, b).tiles(c) == 0);
       }
     }
-    set(a, group, rows, Seq(a, b), 0);
+    set(a, c, Seq(a, b), 0);
     return true;
   }
   __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == n; }
 };
+
+// ---- the kernel for many query rows (mx_attention_tile.cu) -----------------------------------------
+
+constexpr int kMaxTileCtas = 160;
+// Query rows per tile: two 128-row tiles take turns on the tensor cores where there are rows for both
+// (and tensor memory: not with head_dim 256).
+inline int tile_rows(int64_t rows, int dim) { return rows > 128 && dim < 256 ? 256 : 128; }
+cudaError_t run_tile(const AttnArgs& a, cudaStream_t stream, int* launches);
 
 // ---- workspace: one record per thread block, then two partial results per thread block ------------
 
@@ -259,5 +267,120 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, const Seq& s, int t, uin
   return j < 0 || (a.tree ? j < s.count && ((w >> j) & 1) : j <= t);
 }
 
+// ---- joining pieces --------------------------------------------------------------------------------
+
+namespace {
+
+// Joins the pieces of the segment that block blockIdx.x began and did not end: blocks c .. last hold
+// one each.  blockIdx.y: a quarter of the head dimension.  A thread holds four outputs of a row and
+// every K-th piece; the K runs are added up in order.
+template <int D, int R>
+__global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ AttnArgs a, int ctas,
+                                                        float gv) {
+  constexpr int kItems = R * (D / 16);               // float4 outputs of a quarter
+  constexpr int kPer = kItems < 256 ? kItems : 256;  // threads per run
+  constexpr int K = 256 / kPer;
+  __shared__ float4 s_o[K][kPer];
+  __shared__ float s_m[K][kPer], s_l[K][kPer];
+  griddep_wait();
+  griddep_launch_next();
+  const int c = blockIdx.x;
+  const Record rec = reinterpret_cast<const Record*>(a.workspace)[c];
+  if (rec.last < 0) return;
+  const int group = a.heads / a.c.kv_heads;
+  const int count = a.count ? (int)min((int64_t)max(a.count[rec.b], 0), a.tokens) : (int)a.tokens;
+  const int rows = min((int64_t)R, (int64_t)count * group - (int64_t)rec.rt * R);
+  const int n = rec.last - c + 1;
+  for (int i0 = 0; i0 < kItems; i0 += kPer) {
+    const int i = i0 + (int)threadIdx.x % kPer, run = threadIdx.x / kPer;
+    const int r = i / (D / 16), d = blockIdx.y * (D / 4) + 4 * (i % (D / 16));
+    float mx = -INFINITY, l = 0.0f;
+    float4 y = make_float4(0, 0, 0, 0);
+    if (r < rows) {
+      // pieces run * per .. : an order that depends on their number only
+      const int per = (n + K - 1) / K, x1 = min(n, (run + 1) * per);
+      for (int x0 = run * per; x0 < x1; x0 += 4) {
+        float pm[4], pl[4];
+        float4 po[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pm[e] = -INFINITY, pl[e] = 0.0f, po[e] = make_float4(0, 0, 0, 0);
+          if (x0 + e < x1) {
+            const float* p = partial(a, ctas, R, D, 2 * (c + x0 + e) + (x0 + e == 0));
+            pm[e] = p[r], pl[e] = p[R + r];
+            po[e] = *reinterpret_cast<const float4*>(p + 2 * R + r * D + d);
+          }
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mx);
+        const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(mx - mu);
+        l *= f, y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+        mx = mn;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = ex2(pm[e] - mu);
+          l += pl[e] * w;
+          y.x += po[e].x * w, y.y += po[e].y * w, y.z += po[e].z * w, y.w += po[e].w * w;
+        }
+      }
+    }
+    if constexpr (K > 1) {
+      const int j = threadIdx.x % kPer;
+      s_m[run][j] = mx, s_l[run][j] = l, s_o[run][j] = y;
+      __syncthreads();
+      if (run == 0) {
+        float mn = mx;
+#pragma unroll
+        for (int x = 1; x < K; ++x) mn = fmaxf(mn, s_m[x][j]);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        l = 0.0f, y = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < K; ++x) {
+          const float w = ex2(s_m[x][j] - mu);
+          const float4 v = s_o[x][j];
+          l += s_l[x][j] * w;
+          y.x += v.x * w, y.y += v.y * w, y.z += v.z * w, y.w += v.w * w;
+        }
+        mx = mn;
+      }
+    }
+    if (r < rows && run == 0) {
+      const int64_t row = (int64_t)rec.rt * R + r;
+      const int t = (int)(row / group), head = rec.h * group + (int)(row % group);
+      const float f = l == 0.0f ? 0.0f : gv / l;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + row_offset(a.out, rec.b, t, head) +
+                                d) =
+          make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+      if (a.lse && d == 0)
+        a.lse[(rec.b * a.tokens + t) * a.heads + head] =
+            l == 0.0f ? -INFINITY
+                      : ((mx == -INFINITY ? 0.0f : mx) + log2f(l)) * 0.6931471805599453f;
+    }
+    if constexpr (K > 1) __syncthreads();
+  }
+}
+
+// Launches the join behind a kernel of `ctas` blocks (its blocks only read a record where nothing was
+// split).
+template <int D, int R>
+cudaError_t launch_join(const AttnArgs& a, int ctas, int scale_shift, cudaStream_t stream,
+                        int* launches) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 4);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  const uint32_t g = a.c.g_bits[1];
+  const float gv = ldexpf(g >> 10 ? (float)(1024 + (g & 1023)) : (float)g,
+                          (g >> 10 ? (int)(g >> 10) - 25 : -24) + scale_shift);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attention_join<D, R>, a, ctas, gv);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace
 }  // namespace attn
 }  // namespace mxk

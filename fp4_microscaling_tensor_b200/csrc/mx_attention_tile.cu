@@ -1,0 +1,652 @@
+// mx_attention_tile.cu -- attention over the FP4 cache for many query rows (prompt chunks, trees of
+// drafted tokens) on the fifth-generation tensor cores.
+//
+// The formulas are those of mx_cache_attention.cu.  With 128 query rows and more per key/value head the
+// products dominate: 4 D multiply-adds per row and position against 1 + 2 / N bytes per position and
+// dimension.  So K and V are dequantized once per chunk of 128 positions into shared memory (f16,
+// exact) and serve TILES x 128 rows; scores and outputs stay in tensor memory.
+//
+// One thread block per SM, whose warps have one job each:
+//   * 4 warps per 128-row tile: load and scale the queries (f16, 128-byte-swizzled shared memory);
+//     then per chunk, one row per thread: read the scores from tensor memory, mask, weights
+//     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
+//     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
+//   * 4 warps: a chunk's keys, one position per thread, into the K-major B operand of q K^T;
+//   * 4 warps: its values, 8 positions x D / 8 values per thread, transposed into the K-major (along the
+//     positions) B operand of p V: two positions' codes are interleaved as nibbles, so that a conversion
+//     gives f16 pairs along the positions and no data moves between threads;
+//   * 1 warp, one thread: issues the products.  Two tiles take turns: while one tile's weights are
+//     computed, the tensor cores work on the other's.  p comes from tensor memory (A operand).
+// Tensor memory: scores 128 columns per tile (weights overlay them), outputs D columns per tile.
+//
+// Every wait is bounded (mbar_wait below): a block that gives up says so in a device counter
+// (mx_matmul_gave_up), lets its issued products finish, frees its tensor memory and returns; blocks do
+// not wait for one another.
+#include <atomic>
+
+#include "mx_attention.cuh"
+#include "mx_launch.h"
+#include "mx_tc.cuh"
+
+namespace mxk {
+namespace attn {
+
+__device__ unsigned int g_tile_gave_up;
+
+namespace {
+
+constexpr int kChunk = 128;  // positions per chunk
+constexpr int kTileStart = 2;  // Cut::start, in chunks
+constexpr uint32_t kPolls = 1u << 20;
+constexpr float kSlack = 8.0f;
+
+template <int D, int TILES>
+struct Tile {
+  static constexpr int kRows = 128 * TILES;
+  static constexpr int kStages = D == 256 ? 1 : 2;
+  static constexpr int kQ = 128 * D * 2;                // bytes of one tile's queries
+  static constexpr int kK = kChunk * D * 2;             // bytes of a chunk's keys (and values)
+  static constexpr int kSmem = TILES * kQ + 2 * kStages * kK + 1024;
+  static constexpr int kThreads = 32 * (4 * TILES + 9);
+  static constexpr uint32_t kScoreCol = 0, kOutCol = 128 * TILES;
+  static_assert(kOutCol + TILES * D <= 512, "tensor memory");
+  // Instruction descriptors of kind::f16: float32 accumulator (bits 4..5 = 1), A and B f16, K-major,
+  // N / 8 in bits 17..22, M / 16 in bits 24..28.
+  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kChunk >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+};
+
+// True once the barrier's phase with this parity has completed; false after kPolls polls, or once
+// another warp of the block has given up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 255u) == 255u && *gave_up) return false;
+  }
+  *gave_up = 1;
+  return false;
+}
+
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_store() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two scale codes x, y -> f16 pair (x, y) 2^-kScaleShift.  E4M3 by the hardware's conversion; UE5M3 by
+// value (two scales serve 32 or more codes here).
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x, uint32_t y) {
+  if constexpr (FMT == kE4M3) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+        : "=r"(d) : "r"(__byte_perm(x, y, 0x0040)));
+    return d;
+  } else {
+    return pack_f16x2(scale_value((int)x, FMT) * 0x1p-4f, scale_value((int)y, FMT) * 0x1p-4f);
+  }
+}
+
+template <int D, int TILES, int FMT>
+__global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
+    k_attention_tile(const __grid_constant__ AttnArgs a) {
+  using T = Tile<D, TILES>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t s_q = smem_u32(smem), s_k = s_q + TILES * T::kQ, s_v = s_k + S * T::kK;
+  __shared__ uint64_t bars[6 * 2 + 4 * S + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_gave_up;
+  __shared__ int64_t s_scan[T::kThreads / 32];
+  __shared__ Share s_share;
+  volatile int* gave_up = &s_gave_up;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  // barriers: queries in place, scores done, weights in place, outputs done (per tile); keys and values
+  // in place and read (per stage)
+  auto q_full = [&](int t) { return bar(t); };
+  auto s_full = [&](int t) { return bar(2 + t); };
+  auto p_full = [&](int t) { return bar(4 + t); };
+  auto o_full = [&](int t) { return bar(6 + t); };
+  auto k_full = [&](int s) { return bar(12 + s); };
+  auto k_empty = [&](int s) { return bar(12 + S + s); };
+  auto v_full = [&](int s) { return bar(12 + 2 * S + s); };
+  auto v_empty = [&](int s) { return bar(12 + 3 * S + s); };
+  const uint32_t done = bar(12 + 4 * S);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 4);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(o_full(t), 1);
+    }
+    for (int s = 0; s < S; ++s) {
+      mbar_init(k_full(s), 4);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 4);
+      mbar_init(v_empty(s), 1);
+    }
+    mbar_init(done, 1);
+    s_gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  griddep_wait();
+  griddep_launch_next();
+  const Cut cut{T::kRows, group, kChunk, kTileStart};
+  find_share<T::kThreads>(a, cut, cta, ctas, s_scan, &s_share);
+  const Share sh = s_share;
+  Walk k;
+  bool more = k.begin(a, cut, sh);
+  int n = 0, piece = 0;  // chunks and pieces so far
+
+  if (warp < 4 * TILES) {
+    // ---------------- softmax: one query row per thread ----------------
+    const int tile = warp >> 2, r = 32 * (warp & 3) + lane;
+    const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + T::kScoreCol + 128 * tile + t_lane;
+    const uint32_t t_o = tmem + T::kOutCol + D * tile + t_lane;
+    const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
+    Record mine{0, 0, 0, -1, 0};
+    while (more) {
+      const Seq seq(a, k.b);
+      const int rows = seq.count * group, row = k.rt * T::kRows + 128 * tile + r;
+      const bool in = row < rows;
+      const int t = in ? row / group : 0, head = k.h * group + (in ? row % group : 0);
+      float mult;
+      {
+        // the row times a power of two that brings its largest magnitude to [2^14, 2^15), as f16
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) +
+                                                          row_offset(a.q, k.b, t, head));
+        uint32_t mx = 0;
+        const bool live = in && a.scale != 0.0f;
+        if (live) {
+#pragma unroll 8
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = __ldg(src + i);
+            mx = max(mx, max(max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu),
+                                 max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)),
+                             max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu),
+                                 max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu))));
+          }
+        }
+        const int f = mx == 0 || mx >= 0x7F80u ? 0 : 141 - max((int)(mx >> 7), 1);
+        const int f1 = f / 2, f2 = f - f1;
+        const float s1 = __uint_as_float((uint32_t)(127 + f1) << 23);
+        const float s2 = __uint_as_float((uint32_t)(127 + f2) << 23);
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t dst = s_q + tile * T::kQ + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = __ldg(src + i);
+          auto half2 = [&](uint32_t w) {
+            return pack_f16x2(bf16lo(w) * s1 * s2, bf16hi(w) * s1 * s2) ^ (live ? flip : 0u);
+          };
+          st_shared16(dst + (i >> 3) * 16384u + ((((uint32_t)i & 7u) ^ (r & 7u)) << 4), half2(v.x),
+                      half2(v.y), half2(v.z), half2(v.w));
+        }
+        const float gk = fp16_bits_to_float(a.c.g_bits[0]) * (float)(1 << kScaleShift<FMT>);
+        mult = (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * gk * 1.4426950408889634f) *
+               __uint_as_float((uint32_t)(127 - f1) << 23) * __uint_as_float((uint32_t)(127 - f2) << 23);
+        mult = fminf(fmaxf(mult, 0x1p-126f), 0x1p126f);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(tile));
+
+      const uint64_t word = in && a.tree ? a.tree[k.b * a.tokens + t] : 0;
+      const int plain_end = min(k.end, seq.base + 1);
+      const int chunks = k.c1 - k.c0;
+      float m = -INFINITY, mu = 0.0f, lim = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < chunks; ++j) {
+        const int p = (k.c0 + j) * kChunk;
+        // which 16-position groups of the chunk have a page
+        bool page = true;
+        if (lane < kChunk / 16 && p + 16 * lane < k.end)
+          page = a.table.slot(a.c, k.b, p + 16 * lane) >= 0;
+        const uint32_t pages = __ballot_sync(0xffffffffu, page);
+        ok = mbar_wait(s_full(tile), (n + j) & 1, gave_up);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        const bool plain = p + kChunk <= plain_end && pages == 0xffffffffu;
+        // bit i of seen(c): whether this row sees position p + 32 c + i
+        auto seen = [&](int c) -> uint32_t {
+          const int first = p + 32 * c;
+          auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u; };
+          uint32_t w = below(k.end - first);
+          if (a.tree) {
+            const int j0 = first - seq.base;  // the group's first position among the new tokens
+            const uint64_t have = seq.count >= 64 ? ~0ull : (1ull << seq.count) - 1ull;
+            const uint64_t v = word & have;
+            w &= j0 >= 64 ? 0u : j0 >= 0 ? (uint32_t)(v >> j0)
+                 : j0 <= -32 ? ~0u : ((uint32_t)(v << -j0) | below(-j0));
+          } else {
+            w &= below(seq.base + t + 1 - first);
+          }
+          return w & (((pages >> (2 * c)) & 1 ? 0xFFFFu : 0u) |
+                      ((pages >> (2 * c + 1)) & 1 ? 0xFFFF0000u : 0u));
+        };
+        // ---- the chunk's maximum
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc_load32(t_s + 32 * c, v);
+          if (plain) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx = fmaxf(fmaxf(mx, __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
+          } else {
+            const uint32_t w = seen(c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((w >> i) & 1) mx = fmaxf(mx, __uint_as_float(v[i]));
+            __syncwarp();
+          }
+        }
+        const bool grew = mx > lim;
+        if (__any_sync(0xffffffffu, grew)) {
+          float alpha = 1.0f;
+          if (grew) {
+            alpha = m == -INFINITY ? 0.0f : ex2((m - mx) * mult);
+            m = mx;
+            mu = m * mult;
+            lim = m + kSlack / mult;
+            l0 *= alpha;
+            l1 *= alpha;
+          }
+          __syncwarp();
+          if (j > 0) {
+            // (the scores are done, so the products into the outputs issued before them are too)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tc_load32(t_o + 32 * c, v);
+              uint32_t x[16], y[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                x[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                y[i] = __float_as_uint(__uint_as_float(v[16 + i]) * alpha);
+              }
+              tc_store16(t_o + 32 * c, x);
+              tc_store16(t_o + 32 * c + 16, y);
+            }
+          }
+        }
+        __syncwarp();
+        // ---- weights: f16 pairs over the scores that have been read
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], w[16];
+          tc_load32(t_s + 32 * c, v);
+          if (!plain) {
+            const uint32_t s = seen(c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((s >> i) & 1)) v[i] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                make_float2(mult, mult), make_float2(-mu, -mu));
+            const float e0 = ex2(x.x), e1 = ex2(x.y);
+            l0 += e0;
+            l1 += e1;
+            w[i] = pack_f16x2(e0, e1);
+          }
+          __syncwarp();
+          tc_store16(t_s + 16 * c, w);
+        }
+        tc_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(tile));
+      }
+      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(o_full(tile), piece & 1, gave_up))) break;
+      tc_fence_after();
+      const float l = l0 + l1;
+      const bool whole = k.whole();
+      float* part = partial(a, ctas, T::kRows, D, 2 * cta + (k.c0 == 0));
+      const float f = whole ? (l == 0.0f ? 0.0f : gv / l) : 1.0f;
+      uint16_t* out = static_cast<uint16_t*>(a.out.p) + row_offset(a.out, k.b, t, head);
+      const int pr = 128 * tile + r;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        __syncwarp();
+        tc_load32(t_o + 32 * c, v);
+        if (!in) continue;
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(v[i]) * f;
+        // (a row that has seen nothing so far has no weights: zeros times anything)
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(out + 32 * c + i) =
+                make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
+                           pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(part + 2 * T::kRows + (size_t)pr * D + 32 * c + i) =
+                make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        }
+      }
+      if (in) {
+        if (whole) {
+          if (a.lse)
+            a.lse[(k.b * a.tokens + t) * a.heads + head] =
+                l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+        } else {
+          part[pr] = m == -INFINITY ? -INFINITY : mu;
+          part[T::kRows + pr] = l;
+        }
+      }
+      if (k.c0 == 0 && !whole)
+        mine = {k.b, k.h, k.rt, block_of(k.u0 + k.n + kTileStart - 1, sh), 0};
+      tc_fence_before();
+      n += chunks;
+      ++piece;
+      more = k.next(a, cut);
+    }
+    if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta] = mine;
+  } else if (warp < 4 * TILES + 4) {
+    // ---------------- keys: one position per thread ----------------
+    const int pos = 32 * (warp - 4 * TILES) + lane;
+    const uint32_t dst0 = s_k + (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
+    const int log_block = a.c.log_block;
+    while (more) {
+      const int chunks = k.c1 - k.c0;
+      uint4 code[D / 32];
+      uint32_t sc[D / 64];  // the scale bytes of 64 values
+      auto load = [&](int j) {
+        const int p = (k.c0 + j) * kChunk + pos;
+        int64_t row = p < k.end ? a.table.slot(a.c, k.b, p) : -1;
+        const bool has = row >= 0;
+        row = has ? row + ((int64_t)k.h << a.c.page_shift) : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(a.c.codes[0] + row * (D / 2));
+        const uint8_t* ss = a.c.scales[0] + row * (D >> log_block);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) code[i] = has ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          sc[i] = 0;
+          if (has) {
+            if (log_block == 4) sc[i] = __ldg(reinterpret_cast<const uint32_t*>(ss) + i);
+            else if (log_block == 5) {
+              const uint32_t v = __ldg(reinterpret_cast<const uint16_t*>(ss) + i);
+              sc[i] = (v & 0xFFu) * 0x101u | (v >> 8) * 0x1010000u;
+            } else sc[i] = __ldg(ss + ((64 * i) >> log_block)) * 0x1010101u;
+          }
+        }
+      };
+      load(0);
+      bool ok = true;
+      for (int j = 0; j < chunks; ++j) {
+        const int i = n + j, s = i % S;
+        if (i >= S) ok = mbar_wait(k_empty(s), ((i / S) + 1) & 1, gave_up);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const uint32_t dst = dst0 + s * T::kK;
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = code[2 * q + h];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t b = (sc[q] >> (16 * h + 8 * (e >> 1))) & 0xFFu;
+              const uint32_t f = scale_pair<FMT>(b, b);
+              uint32_t x[4];
+              e2m1x8_to_f16(w[e], x);
+              st_shared16(dst + q * 16384u + (((uint32_t)(4 * h + e) ^ (pos & 7u)) << 4),
+                          mul_f16x2(x[0], f), mul_f16x2(x[1], f), mul_f16x2(x[2], f),
+                          mul_f16x2(x[3], f));
+            }
+          }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full(s));
+        if (j + 1 < chunks) load(j + 1);
+      }
+      if (!ok) break;
+      n += chunks;
+      more = k.next(a, cut);
+    }
+  } else if (warp < 4 * TILES + 8) {
+    // ---------------- values: 8 positions x D / 8 values per thread ----------------
+    const int w4 = warp - 4 * TILES - 4;
+    const int oct = lane & 7, half = w4 & 1;             // positions 64 half + 8 oct ..
+    const int run = (lane >> 3) + 4 * (w4 >> 1);         // values (D / 8) run ..
+    constexpr int W = D / 64;                            // code words per position
+    const int log_block = a.c.log_block;
+    while (more) {
+      const int chunks = k.c1 - k.c0;
+      uint32_t code[8][W], sc[8];
+      auto load = [&](int j) {
+        const int p = (k.c0 + j) * kChunk + 64 * half + 8 * oct;
+        int64_t row = p < k.end ? a.table.slot(a.c, k.b, p) : -1;
+        const int have = row >= 0 ? k.end - p : 0;       // positions from p on
+        row = row >= 0 ? row + ((int64_t)k.h << a.c.page_shift) : 0;
+        const uint8_t* src = a.c.codes[1] + row * (D / 2) + (D / 16) * run;
+        const uint8_t* ss = a.c.scales[1] + row * (D >> log_block) + (((D / 8) * run) >> log_block);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool has = i < have;
+          sc[i] = 0;
+#pragma unroll
+          for (int e = 0; e < W; ++e) code[i][e] = 0;
+          if (has) {
+            const uint8_t* at = src + i * (D / 2);
+            if constexpr (W == 1) code[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+            if constexpr (W == 2) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+              code[i][0] = v.x, code[i][1] = v.y;
+            }
+            if constexpr (W == 4) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+              code[i][0] = v.x, code[i][1] = v.y, code[i][2] = v.z, code[i][3] = v.w;
+            }
+            const uint8_t* sp = ss + i * (D >> log_block);
+            if (W == 4 && log_block == 4) sc[i] = __ldg(reinterpret_cast<const uint16_t*>(sp));
+            else sc[i] = __ldg(sp) * 0x101u;
+          }
+        }
+      };
+      load(0);
+      bool ok = true;
+      for (int j = 0; j < chunks; ++j) {
+        const int i = n + j, s = i % S;
+        if (i >= S) ok = mbar_wait(v_empty(s), ((i / S) + 1) & 1, gave_up);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        // row d of the transposed tile: 128 bytes = this half's 64 positions
+        const uint32_t dst = s_v + s * T::kK + half * (D * 128);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          uint32_t ev[4][4], od[4][4];  // [pair of positions][even / odd values 2 i, 2 i + 1]
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t x = code[2 * q][e], y = code[2 * q + 1][e];
+            const int sh = W == 4 ? 8 * (e >> 1) : 0;
+            const uint32_t f = scale_pair<FMT>((sc[2 * q] >> sh) & 0xFFu, (sc[2 * q + 1] >> sh) & 0xFFu);
+            e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[q]);
+            e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[q]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              ev[q][u] = mul_f16x2(ev[q][u], f);
+              od[q][u] = mul_f16x2(od[q][u], f);
+            }
+          }
+          const uint32_t at = dst + (uint32_t)(W * run + e) * 1024u;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            st_shared16(at + (2 * u) * 128u + (((uint32_t)oct ^ (2 * u)) << 4), ev[0][u], ev[1][u],
+                        ev[2][u], ev[3][u]);
+            st_shared16(at + (2 * u + 1) * 128u + (((uint32_t)oct ^ (2 * u + 1)) << 4), od[0][u],
+                        od[1][u], od[2][u], od[3][u]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full(s));
+        if (j + 1 < chunks) load(j + 1);
+      }
+      if (!ok) break;
+      n += chunks;
+      more = k.next(a, cut);
+    }
+  } else {
+    // ---------------- products (one thread) ----------------
+    if (lane == 0) {
+      auto scores = [&](int t, int s) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          tc_mma_f16(tmem + T::kScoreCol + 128 * t,
+                     desc_sw128(s_q + t * T::kQ + (i >> 2) * 16384 + 32 * (i & 3)),
+                     desc_sw128(s_k + s * T::kK + (i >> 2) * 16384 + 32 * (i & 3)), T::kIdescS, i > 0);
+        tc_commit(s_full(t));
+        if (t == TILES - 1) tc_commit(k_empty(s));
+      };
+      while (more && !*gave_up) {
+        const int chunks = k.c1 - k.c0;
+        bool ok = true;
+        for (int t = 0; t < TILES && ok; ++t) ok = mbar_wait(q_full(t), piece & 1, gave_up);
+        ok = ok && mbar_wait(k_full(n % S), (n / S) & 1, gave_up);
+        if (!ok) break;
+        tc_fence_after();
+        for (int t = 0; t < TILES; ++t) scores(t, n % S);
+        for (int j = 0; j < chunks && ok; ++j) {
+          const int i = n + j, s = i % S;
+          for (int t = 0; t < TILES && ok; ++t) {
+            ok = mbar_wait(p_full(t), i & 1, gave_up);
+            if (ok && t == 0) ok = mbar_wait(v_full(s), (i / S) & 1, gave_up);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < kChunk / 16; ++x)
+              tc_mma_f16_ts(tmem + T::kOutCol + D * t, tmem + T::kScoreCol + 128 * t + 8 * x,
+                            desc_sw128(s_v + s * T::kK + (x >> 2) * (D * 128) + 32 * (x & 3)),
+                            T::kIdescO, j > 0 || x > 0);
+            if (t == TILES - 1) tc_commit(v_empty(s));
+            if (j + 1 < chunks) {
+              if (t == 0) ok = mbar_wait(k_full((i + 1) % S), ((i + 1) / S) & 1, gave_up);
+              if (!ok) break;
+              tc_fence_after();
+              scores(t, (i + 1) % S);
+            } else {
+              tc_commit(o_full(t));
+            }
+          }
+        }
+        if (!ok) break;
+        n += chunks;
+        ++piece;
+        more = k.next(a, cut);
+      }
+      tc_commit(done);  // also after giving up: every issued product
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    bool ok = true;
+    int unused = 0;
+    if (lane == 0) ok = mbar_wait(done, 0, &unused);
+    (void)ok;
+    __syncwarp();
+    if (lane == 0 && *gave_up) atomicAdd(&g_tile_gave_up, 1u);
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+}
+
+template <int D, int TILES, int FMT>
+cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  using T = Tile<D, TILES>;
+  static std::atomic<bool> attr[kMaxDevices];
+  auto* kern = k_attention_tile<D, TILES, FMT>;
+  cudaError_t e = allow_dynamic_smem(attr, kern, T::kSmem);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int ctas = sms < kMaxTileCtas ? sms : kMaxTileCtas;
+  e = launch_pdl_smem(kern, ctas, T::kThreads, T::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  return launch_join<D, T::kRows>(a, ctas, kScaleShift<FMT>, stream, launches);
+}
+
+template <int D, int TILES>
+cudaError_t dispatch(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  return a.c.fmt == kUE5M3 ? launch_tile<D, TILES, kUE5M3>(a, stream, launches)
+                           : launch_tile<D, TILES, kE4M3>(a, stream, launches);
+}
+
+}  // namespace
+
+cudaError_t run_tile(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  const bool two = tile_rows(a.tokens * (a.heads / a.c.kv_heads), a.c.head_dim) == 256;
+  switch (a.c.head_dim) {
+    case 64: return two ? dispatch<64, 2>(a, stream, launches) : dispatch<64, 1>(a, stream, launches);
+    case 128: return two ? dispatch<128, 2>(a, stream, launches) : dispatch<128, 1>(a, stream, launches);
+    default: return dispatch<256, 1>(a, stream, launches);
+  }
+}
+
+}  // namespace attn
+
+cudaError_t attention_gave_up(unsigned int* count) {
+  const unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(count, attn::g_tile_gave_up, sizeof(unsigned int));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(attn::g_tile_gave_up, &zero, sizeof(unsigned int));
+  return e;
+}
+
+}  // namespace mxk

@@ -45,6 +45,8 @@ constexpr int kStreamThreads = 32 * kWarps;
 constexpr float kSlack = 8.0f;
 
 
+constexpr int kUnit = 64, kStart = 4;  // of the stream kernel's Cut (start: 0 88, 2 86, 4 83 us for 64
+                                      // sequences of 819 to 8191 positions)
 constexpr int kPart = 32;  // positions computed at a time (more outgrow the instruction cache)
 
 template <int D, int NT>
@@ -604,14 +606,15 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
   griddep_wait();
   griddep_launch_next();
-  find_share<kStreamThreads>(a, group, R, cta, ctas, s_scan, &s_share);
+  const Cut cut{R, group, kUnit, kStart};
+  find_share<kStreamThreads>(a, cut, cta, ctas, s_scan, &s_share);
   const Share sh = s_share;
   Record* rec = reinterpret_cast<Record*>(a.workspace) + cta;
   Record mine{0, 0, 0, -1, 0};
   const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
 
   Walk k;
-  if (k.begin(a, group, R, sh)) {
+  if (k.begin(a, cut, sh)) {
     Stream<D, NT, FMT, N16> w(a, smem_addr(smem) + warp * G::kWarpBytes, smem_addr(s_table));
     w.group = group;
     int p0;
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
       float* part = partial(a, ctas, R, D, 2 * cta + (k.c0 == 0));
       if (k.c0 == 0 && !whole)
         mine = {b, h, k.rt, block_of(k.u0 + k.n + kStart - 1, sh), 0};
-      const bool more = k.next(a, group, R);
+      const bool more = k.next(a, cut);
       if (more) begin();
       __syncthreads();
 
@@ -705,97 +708,9 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   if (threadIdx.x == 0) *rec = mine;
 }
 
-// Joins the pieces of the segment that block blockIdx.x began and did not end: blocks c .. last hold
-// one each.  blockIdx.y: a quarter of the head dimension.  A thread holds four outputs of a row and
-// every K-th piece; the K runs are added up in order.
-template <int D, int R>
-__global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ AttnArgs a, int ctas,
-                                                        float gv) {
-  constexpr int kItems = R * (D / 16);               // float4 outputs of a quarter
-  constexpr int kPer = kItems < 256 ? kItems : 256;  // threads per run
-  constexpr int K = 256 / kPer;
-  __shared__ float4 s_o[K][kPer];
-  __shared__ float s_m[K][kPer], s_l[K][kPer];
-  griddep_wait();
-  griddep_launch_next();
-  const int c = blockIdx.x;
-  const Record rec = reinterpret_cast<const Record*>(a.workspace)[c];
-  if (rec.last < 0) return;
-  const int group = a.heads / a.c.kv_heads;
-  const int count = a.count ? (int)min((int64_t)max(a.count[rec.b], 0), a.tokens) : (int)a.tokens;
-  const int rows = min((int64_t)R, (int64_t)count * group - (int64_t)rec.rt * R);
-  const int n = rec.last - c + 1;
-  for (int i0 = 0; i0 < kItems; i0 += kPer) {
-    const int i = i0 + (int)threadIdx.x % kPer, run = threadIdx.x / kPer;
-    const int r = i / (D / 16), d = blockIdx.y * (D / 4) + 4 * (i % (D / 16));
-    float mx = -INFINITY, l = 0.0f;
-    float4 y = make_float4(0, 0, 0, 0);
-    if (r < rows) {
-      // pieces run * per .. : an order that depends on their number only
-      const int per = (n + K - 1) / K, x1 = min(n, (run + 1) * per);
-      for (int x0 = run * per; x0 < x1; x0 += 4) {
-        float pm[4], pl[4];
-        float4 po[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pm[e] = -INFINITY, pl[e] = 0.0f, po[e] = make_float4(0, 0, 0, 0);
-          if (x0 + e < x1) {
-            const float* p = partial(a, ctas, R, D, 2 * (c + x0 + e) + (x0 + e == 0));
-            pm[e] = p[r], pl[e] = p[R + r];
-            po[e] = *reinterpret_cast<const float4*>(p + 2 * R + r * D + d);
-          }
-        }
-        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mx);
-        const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(mx - mu);
-        l *= f, y.x *= f, y.y *= f, y.z *= f, y.w *= f;
-        mx = mn;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = ex2(pm[e] - mu);
-          l += pl[e] * w;
-          y.x += po[e].x * w, y.y += po[e].y * w, y.z += po[e].z * w, y.w += po[e].w * w;
-        }
-      }
-    }
-    if constexpr (K > 1) {
-      const int j = threadIdx.x % kPer;
-      s_m[run][j] = mx, s_l[run][j] = l, s_o[run][j] = y;
-      __syncthreads();
-      if (run == 0) {
-        float mn = mx;
-#pragma unroll
-        for (int x = 1; x < K; ++x) mn = fmaxf(mn, s_m[x][j]);
-        const float mu = mn == -INFINITY ? 0.0f : mn;
-        l = 0.0f, y = make_float4(0, 0, 0, 0);
-#pragma unroll
-        for (int x = 0; x < K; ++x) {
-          const float w = ex2(s_m[x][j] - mu);
-          const float4 v = s_o[x][j];
-          l += s_l[x][j] * w;
-          y.x += v.x * w, y.y += v.y * w, y.z += v.z * w, y.w += v.w * w;
-        }
-        mx = mn;
-      }
-    }
-    if (r < rows && run == 0) {
-      const int64_t row = (int64_t)rec.rt * R + r;
-      const int t = (int)(row / group), head = rec.h * group + (int)(row % group);
-      const float f = l == 0.0f ? 0.0f : gv / l;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + row_offset(a.out, rec.b, t, head) +
-                                d) =
-          make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-      if (a.lse && d == 0)
-        a.lse[(rec.b * a.tokens + t) * a.heads + head] =
-            l == 0.0f ? -INFINITY
-                      : ((mx == -INFINITY ? 0.0f : mx) + log2f(l)) * 0.6931471805599453f;
-    }
-    if constexpr (K > 1) __syncthreads();
-  }
-}
-
 // Query rows per tile: 8, 16 or 32, as many as there are (a tile's rows share one pass over the
 // cache); 16 at most for head_dim 256, whose accumulators fill the registers.
-int row_tiles(int64_t rows, int dim) {
+int row_groups(int64_t rows, int dim) {
   const int most = dim == 256 ? 2 : 4;
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   return nt < most ? nt : most;
@@ -817,7 +732,7 @@ cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches)
   // never more blocks than units that the table could hold
   const int group = a.heads / a.c.kv_heads;
   const int64_t tiles = (a.tokens * group + 8 * NT - 1) / (8 * NT);
-  const int64_t reach = (a.table.width << a.c.page_shift) / kUnit + 1;
+  const int64_t reach = (a.table.width << a.c.page_shift) / kUnit + 1 + kStart;
   int64_t grid = (int64_t)per_sm * (sms < 160 ? sms : 160);
   const double most = (double)a.batch * a.c.kv_heads * tiles * reach;
   if (most < (double)grid) grid = (int64_t)most;
@@ -825,22 +740,7 @@ cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches)
   e = launch_pdl_smem(kern, ctas, kStreamThreads, smem, stream, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  // the join: its blocks only read a record where nothing was split
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, 4);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  uint32_t gb = a.c.g_bits[1];
-  const float gv = (gb >> 10 ? (1024 + (gb & 1023)) * exp2f((float)(gb >> 10) - 25.0f)
-                             : gb * 0x1p-24f) * (float)(1 << kScaleShift<FMT>);
-  e = cudaLaunchKernelEx(&cfg, k_attention_join<D, 8 * NT>, a, ctas, gv);
-  if (e == cudaSuccess) ++*launches;
-  return e;
+  return launch_join<D, 8 * NT>(a, ctas, kScaleShift<FMT>, stream, launches);
 }
 
 template <int D, int NT>
@@ -854,7 +754,7 @@ cudaError_t dispatch_format(const AttnArgs& a, cudaStream_t stream, int* launche
 
 template <int D>
 cudaError_t dispatch_rows(const AttnArgs& a, cudaStream_t stream, int* launches) {
-  const int nt = row_tiles(a.tokens * (a.heads / a.c.kv_heads), D);
+  const int nt = row_groups(a.tokens * (a.heads / a.c.kv_heads), D);
   if (nt == 1) return dispatch_format<D, 1>(a, stream, launches);
   if constexpr (D < 256) {
     if (nt == 4) return dispatch_format<D, 4>(a, stream, launches);
@@ -865,15 +765,21 @@ cudaError_t dispatch_rows(const AttnArgs& a, cudaStream_t stream, int* launches)
 }  // namespace
 }  // namespace attn
 
+// Above this many query rows per key/value head the products outweigh the reading of the cache.
+static constexpr int kStreamRows = 32;
+
 size_t attention_workspace_bytes(int64_t batch, int64_t tokens, int heads, int kv_heads,
                                  int head_dim) {
   if (batch == 0 || tokens == 0) return 16;
-  const int rows = 8 * attn::row_tiles(tokens * (heads / kv_heads), head_dim);
-  return attn::records_bytes(attn::kMaxStreamCtas) +
-         2 * (size_t)attn::kMaxStreamCtas * attn::partial_floats(rows, head_dim) * 4;
+  const int64_t all = tokens * (heads / kv_heads);
+  const bool tile = all > kStreamRows;
+  const int rows = tile ? attn::tile_rows(all, head_dim) : 8 * attn::row_groups(all, head_dim);
+  const int ctas = tile ? attn::kMaxTileCtas : attn::kMaxStreamCtas;
+  return attn::records_bytes(ctas) + 2 * (size_t)ctas * attn::partial_floats(rows, head_dim) * 4;
 }
 
 cudaError_t run_cache_attention(const AttnArgs& a, cudaStream_t stream, int* launches) {
+  if (a.tokens * (a.heads / a.c.kv_heads) > kStreamRows) return attn::run_tile(a, stream, launches);
   switch (a.c.head_dim) {
     case 64: return attn::dispatch_rows<64>(a, stream, launches);
     case 128: return attn::dispatch_rows<128>(a, stream, launches);

@@ -310,8 +310,9 @@ MX_API mx_status mx_dequant_matmul(const void* a, int64_t m, int64_t k, const ui
                                    const uint16_t* w_global_scale_dev, void* c, mx_dtype ct,
                                    cudaStream_t stream);
 
-/* Number of mx_matmul thread blocks that stopped waiting since the previous call (0 in normal
- * operation), written to *count (host memory); clears the count.  Synchronizes the device. */
+/* Number of thread blocks of mx_matmul, mx_dequant_matmul and mx_cache_attention that stopped waiting
+ * since the previous call (0 in normal operation), written to *count (host memory); clears the
+ * count.  Synchronizes the device. */
 MX_API mx_status mx_matmul_gave_up(unsigned int* count);
 
 /* Test hook (no counterpart in the pages): marks the most recent mx_matmul / mx_matmul_pair launch

@@ -12,6 +12,13 @@ from cache_helpers import (G_ONE, check_attention, fill, i32, normal_bf16, pages
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def nobody_gave_up():
+    """No bounded wait of a tensor-core kernel runs out."""
+    yield
+    assert mx.matmul_gave_up() == 0
+
+
 def setup(lengths, kvh, head_dim, page, block, fmt, rng, device, g=None, sigma=1.0):
     g = g or ((0x0155, 0x2E66) if fmt == mx.UE5M3 else (G_ONE, 0x2E66))
     table, pages = pages_for(lengths, page, 2, rng)
