@@ -8,13 +8,14 @@
 //
 // One thread block per SM, whose warps have one job each:
 //   * 4 warps per 128-row tile: load and scale the queries (f16, 128-byte-swizzled shared memory);
-//     then per chunk, one row per thread: read the scores from tensor memory, mask, weights
+//     then per chunk, one row per thread: read the scores from tensor memory (with two tiles these
+//     warps take 152 registers a thread, the others 104), mask, weights
 //     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
 //     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
 //   * 4 warps: a chunk's keys, one position per thread, into the K-major B operand of q K^T;
-//   * 4 warps: its values, 8 positions x D / 8 values per thread, transposed into the K-major (along the
-//     positions) B operand of p V: two positions' codes are interleaved as nibbles, so that a conversion
-//     gives f16 pairs along the positions and no data moves between threads;
+//   * 3 warps: its values, 8 positions x 8 values per thread at a time, transposed into the K-major
+//     (along the positions) B operand of p V: two positions' codes are interleaved as nibbles, so that a
+//     conversion gives f16 pairs along the positions and no data moves between threads;
 //   * 1 warp, one thread: issues the products.  Two tiles take turns: while one tile's weights are
 //     computed, the tensor cores work on the other's.  p comes from tensor memory (A operand).
 // Tensor memory: scores 128 columns per tile (weights overlay them), outputs D columns per tile.
@@ -37,6 +38,11 @@ namespace {
 
 constexpr int kChunk = 128;  // positions per chunk
 constexpr int kTileStart = 2;  // Cut::start, in chunks
+constexpr int kValueWarps = 3;
+// Registers per thread with two tiles: the block is launched with 512 x 128; the softmax warps take
+// what the others give up.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kOtherRegs = 104;
+static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * kLaunchRegs, "register split");
 constexpr uint32_t kPolls = 1u << 20;
 constexpr float kSlack = 8.0f;
 
@@ -47,7 +53,7 @@ struct Tile {
   static constexpr int kQ = 128 * D * 2;                // bytes of one tile's queries
   static constexpr int kK = kChunk * D * 2;             // bytes of a chunk's keys (and values)
   static constexpr int kSmem = TILES * kQ + 2 * kStages * kK + 1024;
-  static constexpr int kThreads = 32 * (4 * TILES + 9);
+  static constexpr int kThreads = 128 * (TILES + 2);
   static constexpr uint32_t kScoreCol = 0, kOutCol = 128 * TILES;
   static_assert(kOutCol + TILES * D <= 512, "tensor memory");
   // Instruction descriptors of kind::f16: float32 accumulator (bits 4..5 = 1), A and B f16, K-major,
@@ -75,6 +81,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return false;
 }
 
+// True in one lane of the warp, which is converged.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
@@ -84,6 +99,16 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -91,6 +116,27 @@ __device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&r)[1
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// 32 columns of this warp's lanes, complete only after tc_wait_load.
+__device__ __forceinline__ void tc_load32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// (the registers pass through, so that no use of them moves in front of the wait)
+template <int N>
+__device__ __forceinline__ void tc_wait_load(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tc_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -150,7 +196,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(k_full(s), 4);
       mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 4);
+      mbar_init(v_full(s), kValueWarps);
       mbar_init(v_empty(s), 1);
     }
     mbar_init(done, 1);
@@ -180,6 +226,8 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
 
   if (warp < 4 * TILES) {
     // ---------------- softmax: one query row per thread ----------------
+    if constexpr (TILES == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int tile = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + T::kScoreCol + 128 * tile + t_lane;
@@ -236,7 +284,8 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       const uint64_t word = in && a.tree ? a.tree[k.b * a.tokens + t] : 0;
       const int plain_end = min(k.end, seq.base + 1);
       const int chunks = k.c1 - k.c0;
-      float m = -INFINITY, mu = 0.0f, lim = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float m = -INFINITY, mu = 0.0f, lim = -INFINITY;
+      float2 l = make_float2(0.0f, 0.0f);
       bool ok = true;
       for (int j = 0; j < chunks; ++j) {
         const int p = (k.c0 + j) * kChunk;
@@ -266,24 +315,29 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           return w & (((pages >> (2 * c)) & 1 ? 0xFFFFu : 0u) |
                       ((pages >> (2 * c + 1)) & 1 ? 0xFFFF0000u : 0u));
         };
-        // ---- the chunk's maximum
-        float mx = -INFINITY;
+        auto mask = [&](int c, uint32_t* v) {
+          const uint32_t w = seen(c);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tc_load32(t_s + 32 * c, v);
-          if (plain) {
+          for (int i = 0; i < 32; ++i)
+            if (!((w >> i) & 1)) v[i] = 0xFF800000u;
+        };
+        // ---- the chunk's maximum; its first 64 scores stay in registers
+        uint32_t v[64];
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx = fmaxf(fmaxf(mx, __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
-          } else {
-            const uint32_t w = seen(c);
+        for (int h = 1; h >= 0; --h) {
+          tc_load32_async(t_s + 64 * h, v);
+          tc_load32_async(t_s + 64 * h + 32, v + 32);
+          tc_wait_load(v);
+          if (!plain) mask(2 * h, v), mask(2 * h + 1, v + 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((w >> i) & 1) mx = fmaxf(mx, __uint_as_float(v[i]));
-            __syncwarp();
-          }
+          for (int i = 0; i < 64; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx4[e] =
+                  fmaxf(fmaxf(mx4[e], __uint_as_float(v[i + 2 * e])), __uint_as_float(v[i + 2 * e + 1]));
         }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const bool grew = mx > lim;
         if (__any_sync(0xffffffffu, grew)) {
           float alpha = 1.0f;
@@ -292,52 +346,49 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
             m = mx;
             mu = m * mult;
             lim = m + kSlack / mult;
-            l0 *= alpha;
-            l1 *= alpha;
+            l.x *= alpha;
+            l.y *= alpha;
           }
           __syncwarp();
           if (j > 0) {
             // (the scores are done, so the products into the outputs issued before them are too)
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tc_load32(t_o + 32 * c, v);
-              uint32_t x[16], y[16];
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t x[16];
+              tc_load16(t_o + 16 * c, x);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                x[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                y[i] = __float_as_uint(__uint_as_float(v[16 + i]) * alpha);
-              }
-              tc_store16(t_o + 32 * c, x);
-              tc_store16(t_o + 32 * c + 16, y);
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+              tc_store16(t_o + 16 * c, x);
             }
           }
         }
         __syncwarp();
-        // ---- weights: f16 pairs over the scores that have been read
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], w[16];
-          tc_load32(t_s + 32 * c, v);
-          if (!plain) {
-            const uint32_t s = seen(c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((s >> i) & 1)) v[i] = 0xFF800000u;
-          }
+        // ---- weights: f16 pairs over the scores, whose second 64 are read again
+        auto weights = [&](int c, const uint32_t* x) {
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 x = __ffma2_rn(
-                make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                make_float2(mult, mult), make_float2(-mu, -mu));
-            const float e0 = ex2(x.x), e1 = ex2(x.y);
-            l0 += e0;
-            l1 += e1;
-            w[i] = pack_f16x2(e0, e1);
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                  make_float2(mult, mult), make_float2(-mu, -mu));
+            e = make_float2(ex2(e.x), ex2(e.y));
+            l = __fadd2_rn(l, e);
+            w[i] = pack_f16x2(e.x, e.y);
           }
-          __syncwarp();
           tc_store16(t_s + 16 * c, w);
-        }
+        };
+        uint32_t u[32];
+        tc_load32_async(t_s + 64, u);
+        weights(0, v);
+        weights(1, v + 32);
+        tc_load32_async(t_s + 96, v);
+        tc_wait_load(u);
+        if (!plain) mask(2, u);
+        __syncwarp();
+        weights(2, u);
+        tc_wait_load(v);
+        if (!plain) mask(3, v);
+        __syncwarp();
+        weights(3, v);
         tc_wait_store();
         tc_fence_before();
         __syncwarp();
@@ -346,10 +397,10 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       if (!ok) break;
       if (!__all_sync(0xffffffffu, mbar_wait(o_full(tile), piece & 1, gave_up))) break;
       tc_fence_after();
-      const float l = l0 + l1;
+      const float sum = l.x + l.y;
       const bool whole = k.whole();
       float* part = partial(a, ctas, T::kRows, D, 2 * cta + (k.c0 == 0));
-      const float f = whole ? (l == 0.0f ? 0.0f : gv / l) : 1.0f;
+      const float f = whole ? (sum == 0.0f ? 0.0f : gv / sum) : 1.0f;
       uint16_t* out = static_cast<uint16_t*>(a.out.p) + row_offset(a.out, k.b, t, head);
       const int pr = 128 * tile + r;
 #pragma unroll 1
@@ -379,10 +430,10 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         if (whole) {
           if (a.lse)
             a.lse[(k.b * a.tokens + t) * a.heads + head] =
-                l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+                sum == 0.0f ? -INFINITY : (mu + log2f(sum)) * 0.6931471805599453f;
         } else {
           part[pr] = m == -INFINITY ? -INFINITY : mu;
-          part[T::kRows + pr] = l;
+          part[T::kRows + pr] = sum;
         }
       }
       if (k.c0 == 0 && !whole)
@@ -395,6 +446,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta] = mine;
   } else if (warp < 4 * TILES + 4) {
     // ---------------- keys: one position per thread ----------------
+    if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const int pos = 32 * (warp - 4 * TILES) + lane;
     const uint32_t dst0 = s_k + (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
     const int log_block = a.c.log_block;
@@ -456,139 +508,161 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       n += chunks;
       more = k.next(a, cut);
     }
-  } else if (warp < 4 * TILES + 8) {
-    // ---------------- values: 8 positions x D / 8 values per thread ----------------
-    const int w4 = warp - 4 * TILES - 4;
-    const int oct = lane & 7, half = w4 & 1;             // positions 64 half + 8 oct ..
-    const int run = (lane >> 3) + 4 * (w4 >> 1);         // values (D / 8) run ..
-    constexpr int W = D / 64;                            // code words per position
+  } else {
+    if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < 4 * TILES + 4 + kValueWarps) {
+    // ---------------- values: 8 positions x 8 values per thread at a time ----------------
+    // A chunk is D / 16 blocks of 64 positions x 32 values; lane: positions 8 oct .., 8 of the values.
+    const int w3 = warp - 4 * TILES - 4, oct = lane & 7, sub = lane >> 3;
+    constexpr int kBlocks = D / 16;
     const int log_block = a.c.log_block;
     while (more) {
       const int chunks = k.c1 - k.c0;
-      uint32_t code[8][W], sc[8];
-      auto load = [&](int j) {
-        const int p = (k.c0 + j) * kChunk + 64 * half + 8 * oct;
+      struct Block { uint32_t code[8], sc[8]; };
+      auto load = [&](int j, int blk, Block& x) {
+        const int p = (k.c0 + j) * kChunk + 64 * (blk & 1) + 8 * oct, word = 4 * (blk >> 1) + sub;
         int64_t row = p < k.end ? a.table.slot(a.c, k.b, p) : -1;
         const int have = row >= 0 ? k.end - p : 0;       // positions from p on
         row = row >= 0 ? row + ((int64_t)k.h << a.c.page_shift) : 0;
-        const uint8_t* src = a.c.codes[1] + row * (D / 2) + (D / 16) * run;
-        const uint8_t* ss = a.c.scales[1] + row * (D >> log_block) + (((D / 8) * run) >> log_block);
+        const uint8_t* src = a.c.codes[1] + row * (D / 2) + 4 * word;
+        const uint8_t* ss = a.c.scales[1] + row * (D >> log_block) + ((8 * word) >> log_block);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool has = i < have;
-          sc[i] = 0;
-#pragma unroll
-          for (int e = 0; e < W; ++e) code[i][e] = 0;
-          if (has) {
-            const uint8_t* at = src + i * (D / 2);
-            if constexpr (W == 1) code[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-            if constexpr (W == 2) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-              code[i][0] = v.x, code[i][1] = v.y;
-            }
-            if constexpr (W == 4) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
-              code[i][0] = v.x, code[i][1] = v.y, code[i][2] = v.z, code[i][3] = v.w;
-            }
-            const uint8_t* sp = ss + i * (D >> log_block);
-            if (W == 4 && log_block == 4) sc[i] = __ldg(reinterpret_cast<const uint16_t*>(sp));
-            else sc[i] = __ldg(sp) * 0x101u;
-          }
+          x.code[i] = i < have ? __ldg(reinterpret_cast<const uint32_t*>(src + i * (D / 2))) : 0u;
+          x.sc[i] = i < have ? __ldg(ss + i * (D >> log_block)) : 0u;
         }
       };
-      load(0);
       bool ok = true;
-      for (int j = 0; j < chunks; ++j) {
+      auto store = [&](int j, int blk, const Block& x) {
         const int i = n + j, s = i % S;
-        if (i >= S) ok = mbar_wait(v_empty(s), ((i / S) + 1) & 1, gave_up);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        // row d of the transposed tile: 128 bytes = this half's 64 positions
-        const uint32_t dst = s_v + s * T::kK + half * (D * 128);
+        if (blk == w3 && i >= S) {  // this warp's first block of the chunk
+          ok = __all_sync(0xffffffffu, mbar_wait(v_empty(s), ((i / S) + 1) & 1, gave_up));
+          if (!ok) return;
+        }
+        uint32_t ev[4][4], od[4][4];  // [pair of positions][even / odd values 2 i, 2 i + 1]
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          uint32_t ev[4][4], od[4][4];  // [pair of positions][even / odd values 2 i, 2 i + 1]
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t x = code[2 * q][e], y = code[2 * q + 1][e];
-            const int sh = W == 4 ? 8 * (e >> 1) : 0;
-            const uint32_t f = scale_pair<FMT>((sc[2 * q] >> sh) & 0xFFu, (sc[2 * q + 1] >> sh) & 0xFFu);
-            e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[q]);
-            e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[q]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              ev[q][u] = mul_f16x2(ev[q][u], f);
-              od[q][u] = mul_f16x2(od[q][u], f);
-            }
-          }
-          const uint32_t at = dst + (uint32_t)(W * run + e) * 1024u;
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t lo = x.code[2 * q], hi = x.code[2 * q + 1];
+          const uint32_t f = scale_pair<FMT>(x.sc[2 * q], x.sc[2 * q + 1]);
+          e2m1x8_to_f16((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), ev[q]);
+          e2m1x8_to_f16(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), od[q]);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            st_shared16(at + (2 * u) * 128u + (((uint32_t)oct ^ (2 * u)) << 4), ev[0][u], ev[1][u],
-                        ev[2][u], ev[3][u]);
-            st_shared16(at + (2 * u + 1) * 128u + (((uint32_t)oct ^ (2 * u + 1)) << 4), od[0][u],
-                        od[1][u], od[2][u], od[3][u]);
+            ev[q][u] = mul_f16x2(ev[q][u], f);
+            od[q][u] = mul_f16x2(od[q][u], f);
           }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(s));
-        if (j + 1 < chunks) load(j + 1);
+        // row d of the transposed tile: 128 bytes = 64 positions
+        const uint32_t at = s_v + s * T::kK + (blk & 1) * (D * 128) +
+                            (uint32_t)(4 * (blk >> 1) + sub) * 1024u;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          st_shared16(at + (2 * u) * 128u + (((uint32_t)oct ^ (2 * u)) << 4), ev[0][u], ev[1][u],
+                      ev[2][u], ev[3][u]);
+          st_shared16(at + (2 * u + 1) * 128u + (((uint32_t)oct ^ (2 * u + 1)) << 4), od[0][u], od[1][u],
+                      od[2][u], od[3][u]);
+        }
+        if (blk + kValueWarps >= kBlocks) {  // its last one
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full(s));
+        }
+      };
+      // the loads of a block while the one before it is converted
+      int j0 = 0, b0 = w3, j1, b1;
+      auto step = [&](int j, int blk, int& jn, int& bn) {
+        bn = blk + kValueWarps, jn = j;
+        if (bn >= kBlocks) bn = w3, ++jn;
+      };
+      Block x, y;
+      load(0, w3, x);
+#pragma unroll 1
+      while (true) {
+        step(j0, b0, j1, b1);
+        if (j1 < chunks) load(j1, b1, y);
+        store(j0, b0, x);
+        if (!ok || j1 >= chunks) break;
+        x = y, j0 = j1, b0 = b1;
       }
       if (!ok) break;
       n += chunks;
       more = k.next(a, cut);
     }
-  } else {
-    // ---------------- products (one thread) ----------------
-    if (lane == 0) {
+    } else {
+    // ---------------- products (one elected thread; the warp stays together) ----------------
+      const bool one = elect_one();
       auto scores = [&](int t, int s) {
+        if (one) {
+          uint64_t qd = desc_sw128(s_q + t * T::kQ), kd = desc_sw128(s_k + s * T::kK);
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {  // 64 values of the head: 16 KB apart, 32 bytes per step
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          tc_mma_f16(tmem + T::kScoreCol + 128 * t,
-                     desc_sw128(s_q + t * T::kQ + (i >> 2) * 16384 + 32 * (i & 3)),
-                     desc_sw128(s_k + s * T::kK + (i >> 2) * 16384 + 32 * (i & 3)), T::kIdescS, i > 0);
-        tc_commit(s_full(t));
-        if (t == TILES - 1) tc_commit(k_empty(s));
+            for (int x = 0; x < 4; ++x)
+              tc_mma_f16(tmem + T::kScoreCol + 128 * t, qd + 2 * x, kd + 2 * x, T::kIdescS,
+                         c > 0 || x > 0);
+            qd += 16384 >> 4;
+            kd += 16384 >> 4;
+          }
+          tc_commit(s_full(t));
+          if (t == TILES - 1) tc_commit(k_empty(s));
+        }
+        __syncwarp();
       };
-      while (more && !*gave_up) {
+      auto outputs = [&](int t, int s, bool add) {
+        if (one) {
+          uint64_t vd = desc_sw128(s_v + s * T::kK);
+          uint32_t pa = tmem + T::kScoreCol + 128 * t;
+#pragma unroll 1
+          for (int c = 0; c < kChunk / 64; ++c) {  // 64 positions
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              tc_mma_f16_ts(tmem + T::kOutCol + D * t, pa + 8 * x, vd + 2 * x, T::kIdescO,
+                            add || c > 0 || x > 0);
+            pa += 32;
+            vd += (D * 128) >> 4;
+          }
+          if (t == TILES - 1) tc_commit(v_empty(s));
+        }
+        __syncwarp();
+      };
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(b, parity, gave_up));
+      };
+      bool ok = true;
+      while (more && ok) {
         const int chunks = k.c1 - k.c0;
-        bool ok = true;
-        for (int t = 0; t < TILES && ok; ++t) ok = mbar_wait(q_full(t), piece & 1, gave_up);
-        ok = ok && mbar_wait(k_full(n % S), (n / S) & 1, gave_up);
+        for (int t = 0; t < TILES && ok; ++t) ok = wait(q_full(t), piece & 1);
+        ok = ok && wait(k_full(n % S), (n / S) & 1);
         if (!ok) break;
         tc_fence_after();
         for (int t = 0; t < TILES; ++t) scores(t, n % S);
+#pragma unroll 1
         for (int j = 0; j < chunks && ok; ++j) {
           const int i = n + j, s = i % S;
-          for (int t = 0; t < TILES && ok; ++t) {
-            ok = mbar_wait(p_full(t), i & 1, gave_up);
-            if (ok && t == 0) ok = mbar_wait(v_full(s), (i / S) & 1, gave_up);
+#pragma unroll 1
+          for (int t = 0; t < TILES; ++t) {
+            ok = wait(p_full(t), i & 1);
+            if (ok && t == 0) ok = wait(v_full(s), (i / S) & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < kChunk / 16; ++x)
-              tc_mma_f16_ts(tmem + T::kOutCol + D * t, tmem + T::kScoreCol + 128 * t + 8 * x,
-                            desc_sw128(s_v + s * T::kK + (x >> 2) * (D * 128) + 32 * (x & 3)),
-                            T::kIdescO, j > 0 || x > 0);
-            if (t == TILES - 1) tc_commit(v_empty(s));
+            outputs(t, s, j > 0);
             if (j + 1 < chunks) {
-              if (t == 0) ok = mbar_wait(k_full((i + 1) % S), ((i + 1) / S) & 1, gave_up);
+              if (t == 0) ok = wait(k_full((i + 1) % S), ((i + 1) / S) & 1);
               if (!ok) break;
               tc_fence_after();
               scores(t, (i + 1) % S);
-            } else {
+            } else if (one) {
               tc_commit(o_full(t));
             }
           }
         }
-        if (!ok) break;
         n += chunks;
         ++piece;
         more = k.next(a, cut);
       }
-      tc_commit(done);  // also after giving up: every issued product
+      if (one) tc_commit(done);  // also after giving up: every issued product
+      __syncwarp();
     }
-    __syncwarp();
   }
 
   tc_fence_before();
@@ -613,6 +687,14 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream, int* launches) {
   auto* kern = k_attention_tile<D, TILES, FMT>;
   cudaError_t e = allow_dynamic_smem(attr, kern, T::kSmem);
   if (e != cudaSuccess) return e;
+  if (TILES == 2) {
+    // the split of registers holds for this launch's count only
+    static const int regs = [&] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
