@@ -12,10 +12,11 @@
 //     warps take 152 registers a thread, the others 104), mask, weights
 //     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
 //     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
-//   * 4 warps: a chunk's keys, one position per thread, into the K-major B operand of q K^T;
-//   * 3 warps: its values, 8 positions x 8 values per thread at a time, transposed into the K-major
-//     (along the positions) B operand of p V: two positions' codes are interleaved as nibbles, so that a
-//     conversion gives f16 pairs along the positions and no data moves between threads;
+//   * 3 warps: a chunk's keys, 32 values of a position per thread at a time, into the K-major B operand
+//     of q K^T;
+//   * 4 warps: its values, 8 positions x D / 8 values per thread, transposed into the K-major (along the
+//     positions) B operand of p V: two positions' codes are interleaved as nibbles, so that a conversion
+//     gives f16 pairs along the positions and no data moves between threads;
 //   * 1 warp, one thread: issues the products.  Two tiles take turns: while one tile's weights are
 //     computed, the tensor cores work on the other's.  p comes from tensor memory (A operand).
 // Tensor memory: scores 128 columns per tile (weights overlay them), outputs D columns per tile.
@@ -38,7 +39,7 @@ namespace {
 
 constexpr int kChunk = 128;  // positions per chunk
 constexpr int kTileStart = 2;  // Cut::start, in chunks
-constexpr int kValueWarps = 3;
+constexpr int kKeyWarps = 3, kValueWarps = 4;
 // Registers per thread with two tiles: the block is launched with 512 x 128; the softmax warps take
 // what the others give up.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kOtherRegs = 104;
@@ -63,9 +64,12 @@ struct Tile {
 };
 
 // True once the barrier's phase with this parity has completed; false after kPolls polls, or once
-// another warp of the block has given up.
+// another warp of the block has given up.  SLEEP_NS: between polls of waits that are not urgent.
+template <int SLEEP_NS = 0>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kPolls; ++i) {
+    if (SLEEP_NS > 0 && i > 0) __nanosleep(SLEEP_NS);
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -156,6 +160,15 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t x, uint32_t y) {
   }
 }
 
+// What the warps need of the piece that a walk is at.
+struct PieceOf {
+  int64_t b;
+  int h, rt, c0, chunks, end;
+  __device__ __forceinline__ PieceOf() {}
+  __device__ __forceinline__ explicit PieceOf(const Walk& w)
+      : b(w.b), h(w.h), rt(w.rt), c0(w.c0), chunks(w.c1 - w.c0), end(w.end) {}
+};
+
 template <int D, int TILES, int FMT>
 __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     k_attention_tile(const __grid_constant__ AttnArgs a) {
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   __shared__ int s_gave_up;
   __shared__ int64_t s_scan[T::kThreads / 32];
   __shared__ Share s_share;
+  __shared__ Walk s_walk[T::kThreads / 32];
   volatile int* gave_up = &s_gave_up;
   auto bar = [&](int i) { return smem_u32(bars + i); };
   // barriers: queries in place, scores done, weights in place, outputs done (per tile); keys and values
@@ -194,7 +208,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       mbar_init(o_full(t), 1);
     }
     for (int s = 0; s < S; ++s) {
-      mbar_init(k_full(s), 4);
+      mbar_init(k_full(s), kKeyWarps);
       mbar_init(k_empty(s), 1);
       mbar_init(v_full(s), kValueWarps);
       mbar_init(v_empty(s), 1);
@@ -219,9 +233,22 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   griddep_launch_next();
   const Cut cut{T::kRows, group, kChunk, kTileStart};
   find_share<T::kThreads>(a, cut, cta, ctas, s_scan, &s_share);
-  const Share sh = s_share;
-  Walk k;
-  bool more = k.begin(a, cut, sh);
+  // The warp's walk is kept in shared memory (registers are short) and moved on by one lane.
+  Walk& walk = s_walk[warp];
+  auto first_piece = [&] {
+    int any = 0;
+    if (lane == 0) any = walk.begin(a, cut, s_share);
+    any = __shfl_sync(0xffffffffu, any, 0);
+    return any != 0;
+  };
+  auto next_piece = [&] {
+    int any = 0;
+    __syncwarp();
+    if (lane == 0) any = walk.next(a, cut);
+    any = __shfl_sync(0xffffffffu, any, 0);
+    return any != 0;
+  };
+  bool more = first_piece();
   int n = 0, piece = 0;  // chunks and pieces so far
 
   if (warp < 4 * TILES) {
@@ -233,8 +260,9 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     const uint32_t t_s = tmem + T::kScoreCol + 128 * tile + t_lane;
     const uint32_t t_o = tmem + T::kOutCol + D * tile + t_lane;
     const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
-    Record mine{0, 0, 0, -1, 0};
+    if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta].last = -1;
     while (more) {
+      const PieceOf k(walk);
       const Seq seq(a, k.b);
       const int rows = seq.count * group, row = k.rt * T::kRows + 128 * tile + r;
       const bool in = row < rows;
@@ -283,17 +311,24 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
 
       const uint64_t word = in && a.tree ? a.tree[k.b * a.tokens + t] : 0;
       const int plain_end = min(k.end, seq.base + 1);
-      const int chunks = k.c1 - k.c0;
+      const int chunks = k.chunks;
       float m = -INFINITY, mu = 0.0f, lim = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);
       bool ok = true;
+      // the page number of this lane's 16 positions of a chunk (0 where it does not matter), loaded a
+      // chunk ahead: a wait for the table would be in the way of everything else
+      auto page_of = [&](int chunk) {
+        const int at = chunk * kChunk + 16 * lane;
+        return lane < kChunk / 16 && at < k.end
+                   ? __ldg(a.table.pages + k.b * a.table.stride + (at >> a.c.page_shift)) : 0;
+      };
+      int page = page_of(k.c0);
+#pragma unroll 1
       for (int j = 0; j < chunks; ++j) {
         const int p = (k.c0 + j) * kChunk;
         // which 16-position groups of the chunk have a page
-        bool page = true;
-        if (lane < kChunk / 16 && p + 16 * lane < k.end)
-          page = a.table.slot(a.c, k.b, p + 16 * lane) >= 0;
-        const uint32_t pages = __ballot_sync(0xffffffffu, page);
+        const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0 && page < a.c.pages);
+        page = page_of(k.c0 + j + 1);
         ok = mbar_wait(s_full(tile), (n + j) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
@@ -315,12 +350,21 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           return w & (((pages >> (2 * c)) & 1 ? 0xFFFFu : 0u) |
                       ((pages >> (2 * c + 1)) & 1 ? 0xFFFF0000u : 0u));
         };
-        auto mask = [&](int c, uint32_t* v) {
-          const uint32_t w = seen(c);
+        if (!plain) {
+          // boundary chunks (few): the scores that this row does not see become -infinity in place
+#pragma unroll 1
+          for (int c = 0; c < kChunk / 16; ++c) {
+            uint32_t x[16];
+            tc_load16(t_s + 16 * c, x);
+            const uint32_t w = seen(c >> 1) >> (16 * (c & 1));
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((w >> i) & 1)) v[i] = 0xFF800000u;
-        };
+            for (int i = 0; i < 16; ++i)
+              if (!((w >> i) & 1)) x[i] = 0xFF800000u;
+            __syncwarp();
+            tc_store16(t_s + 16 * c, x);
+          }
+          tc_wait_store();
+        }
         // ---- the chunk's maximum; its first 64 scores stay in registers
         uint32_t v[64];
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -329,7 +373,6 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           tc_load32_async(t_s + 64 * h, v);
           tc_load32_async(t_s + 64 * h + 32, v + 32);
           tc_wait_load(v);
-          if (!plain) mask(2 * h, v), mask(2 * h + 1, v + 32);
 #pragma unroll
           for (int i = 0; i < 64; i += 8)
 #pragma unroll
@@ -376,19 +419,14 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           tc_store16(t_s + 16 * c, w);
         };
-        uint32_t u[32];
-        tc_load32_async(t_s + 64, u);
         weights(0, v);
+        tc_load32_async(t_s + 64, v);
         weights(1, v + 32);
-        tc_load32_async(t_s + 96, v);
-        tc_wait_load(u);
-        if (!plain) mask(2, u);
-        __syncwarp();
-        weights(2, u);
         tc_wait_load(v);
-        if (!plain) mask(3, v);
-        __syncwarp();
-        weights(3, v);
+        tc_load32_async(t_s + 96, v + 32);
+        weights(2, v);
+        tc_wait_load(v);
+        weights(3, v + 32);
         tc_wait_store();
         tc_fence_before();
         __syncwarp();
@@ -398,31 +436,30 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(o_full(tile), piece & 1, gave_up))) break;
       tc_fence_after();
       const float sum = l.x + l.y;
-      const bool whole = k.whole();
+      const bool whole = walk.whole();
       float* part = partial(a, ctas, T::kRows, D, 2 * cta + (k.c0 == 0));
       const float f = whole ? (sum == 0.0f ? 0.0f : gv / sum) : 1.0f;
       uint16_t* out = static_cast<uint16_t*>(a.out.p) + row_offset(a.out, k.b, t, head);
       const int pr = 128 * tile + r;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t x[16];
         __syncwarp();
-        tc_load32(t_o + 32 * c, v);
+        tc_load16(t_o + 16 * c, x);
         if (!in) continue;
-        float y[32];
+        float y[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(v[i]) * f;
-        // (a row that has seen nothing so far has no weights: zeros times anything)
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(x[i]) * f;
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(out + 32 * c + i) =
+          for (int i = 0; i < 16; i += 8)
+            *reinterpret_cast<uint4*>(out + 16 * c + i) =
                 make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
                            pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(part + 2 * T::kRows + (size_t)pr * D + 32 * c + i) =
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(part + 2 * T::kRows + (size_t)pr * D + 16 * c + i) =
                 make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
         }
       }
@@ -436,157 +473,185 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           part[T::kRows + pr] = sum;
         }
       }
-      if (k.c0 == 0 && !whole)
-        mine = {k.b, k.h, k.rt, block_of(k.u0 + k.n + kTileStart - 1, sh), 0};
+      if (threadIdx.x == 0 && k.c0 == 0 && !whole)
+        reinterpret_cast<Record*>(a.workspace)[cta] = {
+            k.b, k.h, k.rt, block_of(walk.u0 + walk.n + kTileStart - 1, s_share), 0};
       tc_fence_before();
       n += chunks;
       ++piece;
-      more = k.next(a, cut);
+      more = next_piece();
     }
-    if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta] = mine;
-  } else if (warp < 4 * TILES + 4) {
-    // ---------------- keys: one position per thread ----------------
+  } else {
     if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    const int pos = 32 * (warp - 4 * TILES) + lane;
-    const uint32_t dst0 = s_k + (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
-    const int log_block = a.c.log_block;
+    const int log_block = a.c.log_block, log_sb = log2_of(D) - log_block;
+    PieceOf k;
+    // Lane i < 8 gets the place of the chunk's positions 16 i ..: the row of the cache (slots of one
+    // head) divided by 16, or -1.
+    auto page_rows = [&](int chunk) {
+      const int p = chunk * kChunk + 16 * lane;
+      int row = -1;
+      if (lane < kChunk / 16 && p < k.end) {
+        const int64_t slot = a.table.slot(a.c, k.b, p);
+        if (slot >= 0) row = (int)((slot + ((int64_t)k.h << a.c.page_shift)) >> 4);
+      }
+      return row;
+    };
+    if (warp < 4 * TILES + kValueWarps) {
+    // ---------------- values: 8 positions x D / 8 values per thread ----------------
+    const int w4 = warp - 4 * TILES;
+    const int oct = lane & 7, half = w4 & 1;             // positions 64 half + 8 oct ..
+    const int run = (lane >> 3) + 4 * (w4 >> 1);         // values (D / 8) run ..
+    constexpr int W = D / 64;                            // code words per position
+    const uint8_t* src0 = a.c.codes[1] + (oct & 1) * (8 * (D / 2)) + (D / 16) * run;
+    const uint8_t* ss0 = a.c.scales[1] + ((8 * (oct & 1)) << log_sb) + (((D / 8) * run) >> log_block);
     while (more) {
-      const int chunks = k.c1 - k.c0;
-      uint4 code[D / 32];
-      uint32_t sc[D / 64];  // the scale bytes of 64 values
+      k = PieceOf(walk);
+      const int chunks = k.chunks;
+      uint32_t code[8][W], sc[8];
+      int rows = page_rows(k.c0);
       auto load = [&](int j) {
-        const int p = (k.c0 + j) * kChunk + pos;
-        int64_t row = p < k.end ? a.table.slot(a.c, k.b, p) : -1;
-        const bool has = row >= 0;
-        row = has ? row + ((int64_t)k.h << a.c.page_shift) : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(a.c.codes[0] + row * (D / 2));
-        const uint8_t* ss = a.c.scales[0] + row * (D >> log_block);
+        const int p = (k.c0 + j) * kChunk + 64 * half + 8 * oct;
+        const int row = __shfl_sync(0xffffffffu, rows, 4 * half + (oct >> 1));
+        const int have = row >= 0 ? k.end - p : 0;       // positions from p on
+        const uint8_t* src = src0 + (uint64_t)(uint32_t)max(row, 0) * (16 * (D / 2));
+        const uint8_t* ss = ss0 + ((uint64_t)(uint32_t)max(row, 0) << (4 + log_sb));
+        rows = page_rows(k.c0 + j + 1);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) code[i] = has ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
+        for (int i = 0; i < 8; ++i) {
           sc[i] = 0;
-          if (has) {
-            if (log_block == 4) sc[i] = __ldg(reinterpret_cast<const uint32_t*>(ss) + i);
-            else if (log_block == 5) {
-              const uint32_t v = __ldg(reinterpret_cast<const uint16_t*>(ss) + i);
-              sc[i] = (v & 0xFFu) * 0x101u | (v >> 8) * 0x1010000u;
-            } else sc[i] = __ldg(ss + ((64 * i) >> log_block)) * 0x1010101u;
+#pragma unroll
+          for (int e = 0; e < W; ++e) code[i][e] = 0;
+          if (i < have) {
+            const uint8_t* at = src + i * (D / 2);
+            if constexpr (W == 1) code[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+            if constexpr (W == 2) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+              code[i][0] = v.x, code[i][1] = v.y;
+            }
+            if constexpr (W == 4) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+              code[i][0] = v.x, code[i][1] = v.y, code[i][2] = v.z, code[i][3] = v.w;
+            }
+            const uint8_t* sp = ss + (i << log_sb);
+            if (W == 4 && log_block == 4) sc[i] = __ldg(reinterpret_cast<const uint16_t*>(sp));
+            else sc[i] = W == 4 ? __ldg(sp) * 0x101u : __ldg(sp);
           }
         }
       };
       load(0);
       bool ok = true;
+#pragma unroll 1
       for (int j = 0; j < chunks; ++j) {
         const int i = n + j, s = i % S;
-        if (i >= S) ok = mbar_wait(k_empty(s), ((i / S) + 1) & 1, gave_up);
+        if (i >= S) ok = mbar_wait<40>(v_empty(s), ((i / S) + 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const uint32_t dst = dst0 + s * T::kK;
+        // row d of the transposed tile: 128 bytes = this half's 64 positions
+        const uint32_t dst = s_v + s * T::kK + half * (D * 128);
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q)
+        for (int e = 0; e < W; ++e) {
+          uint32_t ev[4][4], od[4][4];  // [pair of positions][even / odd values 2 i, 2 i + 1]
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 v = code[2 * q + h];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t x = code[2 * q][e], y = code[2 * q + 1][e];
+            const uint32_t f =
+                W == 4 ? scale_pair<FMT>((sc[2 * q] >> (8 * (e >> 1))) & 0xFFu,
+                                         (sc[2 * q + 1] >> (8 * (e >> 1))) & 0xFFu)
+                       : scale_pair<FMT>(sc[2 * q], sc[2 * q + 1]);
+            e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[q]);
+            e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[q]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t b = (sc[q] >> (16 * h + 8 * (e >> 1))) & 0xFFu;
-              const uint32_t f = scale_pair<FMT>(b, b);
-              uint32_t x[4];
-              e2m1x8_to_f16(w[e], x);
-              st_shared16(dst + q * 16384u + (((uint32_t)(4 * h + e) ^ (pos & 7u)) << 4),
-                          mul_f16x2(x[0], f), mul_f16x2(x[1], f), mul_f16x2(x[2], f),
-                          mul_f16x2(x[3], f));
+            for (int u = 0; u < 4; ++u) {
+              ev[q][u] = mul_f16x2(ev[q][u], f);
+              od[q][u] = mul_f16x2(od[q][u], f);
             }
           }
+          const uint32_t at = dst + (uint32_t)(W * run + e) * 1024u;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            st_shared16(at + (2 * u) * 128u + (((uint32_t)oct ^ (2 * u)) << 4), ev[0][u], ev[1][u],
+                        ev[2][u], ev[3][u]);
+            st_shared16(at + (2 * u + 1) * 128u + (((uint32_t)oct ^ (2 * u + 1)) << 4), od[0][u],
+                        od[1][u], od[2][u], od[3][u]);
+          }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(s));
+        if (lane == 0) mbar_arrive(v_full(s));
         if (j + 1 < chunks) load(j + 1);
       }
       if (!ok) break;
       n += chunks;
-      more = k.next(a, cut);
+      more = next_piece();
     }
-  } else {
-    if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < 4 * TILES + 4 + kValueWarps) {
-    // ---------------- values: 8 positions x 8 values per thread at a time ----------------
-    // A chunk is D / 16 blocks of 64 positions x 32 values; lane: positions 8 oct .., 8 of the values.
-    const int w3 = warp - 4 * TILES - 4, oct = lane & 7, sub = lane >> 3;
-    constexpr int kBlocks = D / 16;
-    const int log_block = a.c.log_block;
+    } else if (warp < 4 * TILES + kValueWarps + kKeyWarps) {
+    // ---------------- keys: blocks of 32 positions x 32 values, one position per lane ----------------
+    const int w3 = warp - 4 * TILES - kValueWarps;
+    constexpr int kBlocks = D / 8;
     while (more) {
-      const int chunks = k.c1 - k.c0;
-      struct Block { uint32_t code[8], sc[8]; };
-      auto load = [&](int j, int blk, Block& x) {
-        const int p = (k.c0 + j) * kChunk + 64 * (blk & 1) + 8 * oct, word = 4 * (blk >> 1) + sub;
-        int64_t row = p < k.end ? a.table.slot(a.c, k.b, p) : -1;
-        const int have = row >= 0 ? k.end - p : 0;       // positions from p on
-        row = row >= 0 ? row + ((int64_t)k.h << a.c.page_shift) : 0;
-        const uint8_t* src = a.c.codes[1] + row * (D / 2) + 4 * word;
-        const uint8_t* ss = a.c.scales[1] + row * (D >> log_block) + ((8 * word) >> log_block);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x.code[i] = i < have ? __ldg(reinterpret_cast<const uint32_t*>(src + i * (D / 2))) : 0u;
-          x.sc[i] = i < have ? __ldg(ss + i * (D >> log_block)) : 0u;
+      k = PieceOf(walk);
+      const int chunks = k.chunks;
+      int rows = page_rows(k.c0), rows_next = page_rows(k.c0 + 1);
+      struct Block { uint4 code; uint32_t sc; };
+      // the place of a block: chunk lj, block lb; loads run two blocks ahead of the conversions
+      int lj = 0, lb = w3;
+      auto load = [&](Block& x) {
+        x.code = make_uint4(0, 0, 0, 0);
+        x.sc = 0;
+        if (lj >= chunks) return;
+        const int quarter = lb & 3, piece = lb >> 2;
+        const int row = __shfl_sync(0xffffffffu, rows, 2 * quarter + (lane >> 4));
+        if (row >= 0 && (k.c0 + lj) * kChunk + 32 * quarter + lane < k.end) {
+          const uint64_t at = (uint64_t)row * 16 + (lane & 15);
+          x.code = __ldg(reinterpret_cast<const uint4*>(a.c.codes[0] + at * (D / 2)) + piece);
+          const uint8_t* sp = a.c.scales[0] + (at << log_sb) + ((32 * piece) >> log_block);
+          if (log_block == 4) x.sc = __ldg(reinterpret_cast<const uint16_t*>(sp));
+          else x.sc = __ldg(sp) * 0x101u;
+        }
+        __syncwarp();
+        lb += kKeyWarps;
+        if (lb >= kBlocks) {
+          lb = w3;
+          ++lj;
+          rows = rows_next;
+          rows_next = page_rows(k.c0 + lj + 1);
         }
       };
+      Block x0, x1, x2;
+      load(x0);
+      load(x1);
       bool ok = true;
-      auto store = [&](int j, int blk, const Block& x) {
-        const int i = n + j, s = i % S;
-        if (blk == w3 && i >= S) {  // this warp's first block of the chunk
-          ok = __all_sync(0xffffffffu, mbar_wait(v_empty(s), ((i / S) + 1) & 1, gave_up));
-          if (!ok) return;
-        }
-        uint32_t ev[4][4], od[4][4];  // [pair of positions][even / odd values 2 i, 2 i + 1]
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t lo = x.code[2 * q], hi = x.code[2 * q + 1];
-          const uint32_t f = scale_pair<FMT>(x.sc[2 * q], x.sc[2 * q + 1]);
-          e2m1x8_to_f16((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), ev[q]);
-          e2m1x8_to_f16(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), od[q]);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            ev[q][u] = mul_f16x2(ev[q][u], f);
-            od[q][u] = mul_f16x2(od[q][u], f);
-          }
-        }
-        // row d of the transposed tile: 128 bytes = 64 positions
-        const uint32_t at = s_v + s * T::kK + (blk & 1) * (D * 128) +
-                            (uint32_t)(4 * (blk >> 1) + sub) * 1024u;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          st_shared16(at + (2 * u) * 128u + (((uint32_t)oct ^ (2 * u)) << 4), ev[0][u], ev[1][u],
-                      ev[2][u], ev[3][u]);
-          st_shared16(at + (2 * u + 1) * 128u + (((uint32_t)oct ^ (2 * u + 1)) << 4), od[0][u], od[1][u],
-                      od[2][u], od[3][u]);
-        }
-        if (blk + kValueWarps >= kBlocks) {  // its last one
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_full(s));
-        }
-      };
-      // the loads of a block while the one before it is converted
-      int j0 = 0, b0 = w3, j1, b1;
-      auto step = [&](int j, int blk, int& jn, int& bn) {
-        bn = blk + kValueWarps, jn = j;
-        if (bn >= kBlocks) bn = w3, ++jn;
-      };
-      Block x, y;
-      load(0, w3, x);
 #pragma unroll 1
-      while (true) {
-        step(j0, b0, j1, b1);
-        if (j1 < chunks) load(j1, b1, y);
-        store(j0, b0, x);
-        if (!ok || j1 >= chunks) break;
-        x = y, j0 = j1, b0 = b1;
+      for (int j = 0; j < chunks; ++j) {
+        const int i = n + j, s = i % S;
+        if (i >= S) ok = mbar_wait<40>(k_empty(s), ((i / S) + 1) & 1, gave_up);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+#pragma unroll 1
+        for (int blk = w3; blk < kBlocks; blk += kKeyWarps) {
+          load(x2);
+          const int piece = blk >> 2, pos = 32 * (blk & 3) + lane;
+          const uint32_t dst = s_k + s * T::kK + (uint32_t)(piece >> 1) * 16384u +
+                               (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
+          const uint32_t w[4] = {x0.code.x, x0.code.y, x0.code.z, x0.code.w};
+          const uint32_t f2 = scale_pair<FMT>(x0.sc & 0xFFu, x0.sc >> 8);
+          const uint32_t f[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x[4];
+            e2m1x8_to_f16(w[e], x);
+            st_shared16(dst + (((uint32_t)(4 * (piece & 1) + e) ^ (pos & 7u)) << 4),
+                        mul_f16x2(x[0], f[e >> 1]), mul_f16x2(x[1], f[e >> 1]),
+                        mul_f16x2(x[2], f[e >> 1]), mul_f16x2(x[3], f[e >> 1]));
+          }
+          x0 = x1;
+          x1 = x2;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full(s));
       }
       if (!ok) break;
       n += chunks;
-      more = k.next(a, cut);
+      more = next_piece();
     }
     } else {
     // ---------------- products (one elected thread; the warp stays together) ----------------
@@ -630,7 +695,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       };
       bool ok = true;
       while (more && ok) {
-        const int chunks = k.c1 - k.c0;
+        const int chunks = walk.c1 - walk.c0;
         for (int t = 0; t < TILES && ok; ++t) ok = wait(q_full(t), piece & 1);
         ok = ok && wait(k_full(n % S), (n / S) & 1);
         if (!ok) break;
@@ -658,7 +723,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         }
         n += chunks;
         ++piece;
-        more = k.next(a, cut);
+        more = next_piece();
       }
       if (one) tc_commit(done);  // also after giving up: every issued product
       __syncwarp();
