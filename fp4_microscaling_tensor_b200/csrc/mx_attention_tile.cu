@@ -3,23 +3,27 @@
 //
 // The formulas are those of mx_cache_attention.cu.  With 128 query rows and more per key/value head the
 // products dominate: 4 D multiply-adds per row and position against 1 + 2 / N bytes per position and
-// dimension.  So K and V are dequantized once per chunk of 128 positions into shared memory (f16,
+// dimension.  So K and V are dequantized once per chunk of 64 positions into shared memory (f16,
 // exact) and serve TILES x 128 rows; scores and outputs stay in tensor memory.
 //
 // One thread block per SM, whose warps have one job each:
 //   * 4 warps per 128-row tile: load and scale the queries (f16, 128-byte-swizzled shared memory);
-//     then per chunk, one row per thread: read the scores from tensor memory (with two tiles these
-//     warps take 152 registers a thread, the others 104), mask, weights
+//     then per chunk, one row per thread: read the scores from tensor memory, mask, weights
 //     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
 //     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
-//   * 3 warps: a chunk's keys, 32 values of a position per thread at a time, into the K-major B operand
-//     of q K^T;
-//   * 4 warps: its values, 8 positions x D / 8 values per thread, transposed into the K-major (along the
-//     positions) B operand of p V: two positions' codes are interleaved as nibbles, so that a conversion
-//     gives f16 pairs along the positions and no data moves between threads;
-//   * 1 warp, one thread: issues the products.  Two tiles take turns: while one tile's weights are
-//     computed, the tensor cores work on the other's.  p comes from tensor memory (A operand).
-// Tensor memory: scores 128 columns per tile (weights overlay them), outputs D columns per tile.
+//   * 1 warp: brings the chunks' codes and scales into a ring in shared memory (bulk copies), up to
+//     three chunks ahead;
+//   * 2 warps: a chunk's keys, one position per thread, into the K-major B operand of q K^T;
+//   * 4 warps: its values (two of them every other chunk), 8 positions x D / 8 values per thread,
+//     transposed into the K-major (along the positions) B operand of p V: two positions' codes are
+//     interleaved as nibbles, so that a conversion gives f16 pairs along the positions and no data moves
+//     between threads;
+//   * 1 warp, one thread: issues the products: a tile's scores of the next chunk before its outputs of
+//     this one, so that its softmax warps always have scores to go on with.  p comes from tensor memory
+//     (A operand).
+// Tensor memory per tile: two buffers of 64 columns of scores (weights overlay them), D columns of
+// outputs.  (Chunks of 128 positions with one buffer per tile left the softmax waiting for its own
+// products: 1158 us for 2048 prompt tokens over 16384 positions, 64 heads on 8, against 0.)
 //
 // Every wait is bounded (mbar_wait below): a block that gives up says so in a device counter
 // (mx_matmul_gave_up), lets its issued products finish, frees its tensor memory and returns; blocks do
@@ -37,25 +41,28 @@ __device__ unsigned int g_tile_gave_up;
 
 namespace {
 
-constexpr int kChunk = 128;  // positions per chunk
-constexpr int kTileStart = 2;  // Cut::start, in chunks
-constexpr int kKeyWarps = 3, kValueWarps = 4;
-// Registers per thread with two tiles: the block is launched with 512 x 128; the softmax warps take
-// what the others give up.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kOtherRegs = 104;
-static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * kLaunchRegs, "register split");
+constexpr int kChunk = 64;  // positions per chunk
+constexpr int kTileStart = 4;  // Cut::start, in chunks
+constexpr int kKeyWarps = 2, kValueWarps = 4;
 constexpr uint32_t kPolls = 1u << 20;
 constexpr float kSlack = 8.0f;
 
 template <int D, int TILES>
 struct Tile {
   static constexpr int kRows = 128 * TILES;
-  static constexpr int kStages = D == 256 ? 1 : 2;
+  static constexpr int kStages = D == 256 ? 2 : 4;
   static constexpr int kQ = 128 * D * 2;                // bytes of one tile's queries
   static constexpr int kK = kChunk * D * 2;             // bytes of a chunk's keys (and values)
-  static constexpr int kSmem = TILES * kQ + 2 * kStages * kK + 1024;
+  // ring of codes and scales: keys, values (8 positions at a time, 16 bytes apart, so that the threads
+  // of 8 runs of 8 positions read different banks), their scales (at most one per 16 values)
+  static constexpr int kRing = D == 256 ? 1 : 3;
+  static constexpr int kOctet = 8 * (D / 2) + 16;
+  static constexpr int kRawV = kChunk * (D / 2), kRawKS = kRawV + kChunk / 8 * kOctet,
+                       kRawVS = kRawKS + kChunk * (D / 16), kRaw = kRawVS + kChunk * (D / 16);
+  static constexpr int kSmem = TILES * kQ + 2 * kStages * kK + kRing * kRaw + 1024;
+  static_assert(kSmem <= 230000, "shared memory");
   static constexpr int kThreads = 128 * (TILES + 2);
-  static constexpr uint32_t kScoreCol = 0, kOutCol = 128 * TILES;
+  static constexpr uint32_t kScoreCol = 0, kOutCol = 2 * kChunk * TILES;
   static_assert(kOutCol + TILES * D <= 512, "tensor memory");
   // Instruction descriptors of kind::f16: float32 accumulator (bits 4..5 = 1), A and B f16, K-major,
   // N / 8 in bits 17..22, M / 16 in bits 24..28.
@@ -85,6 +92,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return false;
 }
 
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // True in one lane of the warp, which is converged.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -94,13 +114,28 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                              uint32_t accumulate) {
+// Shared-memory operands are named by the low word of their descriptor (desc_sw128): the high word is
+// the same for all of them, and the fewer registers an issue has to move, the faster it is.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+// d (+)= a b with a in shared memory, or in tensor memory (f16 pairs).
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "r"((uint32_t)add)
       : "memory");
 }
 __device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -177,8 +212,11 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const uint32_t s_q = smem_u32(smem), s_k = s_q + TILES * T::kQ, s_v = s_k + S * T::kK;
-  __shared__ uint64_t bars[6 * 2 + 4 * S + 1];
+  const uint32_t s_q = smem_u32(smem), s_k = s_q + TILES * T::kQ, s_v = s_k + S * T::kK,
+                 s_raw = s_v + S * T::kK;
+  constexpr int R = T::kRing;
+  __shared__ uint64_t bars[14 + 4 * S + 2 * R + 1];
+  __shared__ uint32_t s_pages[R];  // which 16 positions of the ring's chunks have a page
   __shared__ uint32_t tmem_slot;
   __shared__ int s_gave_up;
   __shared__ int64_t s_scan[T::kThreads / 32];
@@ -186,32 +224,43 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   __shared__ Walk s_walk[T::kThreads / 32];
   volatile int* gave_up = &s_gave_up;
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  // barriers: queries in place, scores done, weights in place, outputs done (per tile); keys and values
-  // in place and read (per stage)
+  // barriers: per tile, queries in place, and for every other chunk, scores done, weights in place,
+  // outputs done; per stage, keys and values in place and read; per place of the ring, codes in place and
+  // read.  (A wait by parity is sound where the
+  // phase before the awaited one is known to be over and the one behind it cannot end before the wait
+  // does; softmax and products may be two chunks apart, so the chunks' barriers come in pairs.)
   auto q_full = [&](int t) { return bar(t); };
-  auto s_full = [&](int t) { return bar(2 + t); };
-  auto p_full = [&](int t) { return bar(4 + t); };
-  auto o_full = [&](int t) { return bar(6 + t); };
-  auto k_full = [&](int s) { return bar(12 + s); };
-  auto k_empty = [&](int s) { return bar(12 + S + s); };
-  auto v_full = [&](int s) { return bar(12 + 2 * S + s); };
-  auto v_empty = [&](int s) { return bar(12 + 3 * S + s); };
-  const uint32_t done = bar(12 + 4 * S);
+  auto o_done = [&](int t, int buf) { return bar(2 + 2 * t + buf); };
+  auto s_full = [&](int t, int buf) { return bar(6 + 2 * t + buf); };
+  auto p_full = [&](int t, int buf) { return bar(10 + 2 * t + buf); };
+  auto k_full = [&](int s) { return bar(14 + s); };
+  auto k_empty = [&](int s) { return bar(14 + S + s); };
+  auto v_full = [&](int s) { return bar(14 + 2 * S + s); };
+  auto v_empty = [&](int s) { return bar(14 + 3 * S + s); };
+  auto raw_full = [&](int r) { return bar(14 + 4 * S + r); };
+  auto raw_empty = [&](int r) { return bar(14 + 4 * S + R + r); };
+  const uint32_t done = bar(14 + 4 * S + 2 * R);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 4);
-      mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);
-      mbar_init(o_full(t), 1);
+      for (int buf = 0; buf < 2; ++buf) {
+        mbar_init(o_done(t, buf), 1);
+        mbar_init(s_full(t, buf), 1);
+        mbar_init(p_full(t, buf), 4);
+      }
     }
     for (int s = 0; s < S; ++s) {
       mbar_init(k_full(s), kKeyWarps);
       mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), kValueWarps);
+      mbar_init(v_full(s), kValueWarps / 2);
       mbar_init(v_empty(s), 1);
+    }
+    for (int r = 0; r < R; ++r) {
+      mbar_init(raw_full(r), 1);
+      mbar_init(raw_empty(r), kKeyWarps + kValueWarps);
     }
     mbar_init(done, 1);
     s_gave_up = 0;
@@ -238,6 +287,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   auto first_piece = [&] {
     int any = 0;
     if (lane == 0) any = walk.begin(a, cut, s_share);
+    __syncwarp();
     any = __shfl_sync(0xffffffffu, any, 0);
     return any != 0;
   };
@@ -245,6 +295,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     int any = 0;
     __syncwarp();
     if (lane == 0) any = walk.next(a, cut);
+    __syncwarp();
     any = __shfl_sync(0xffffffffu, any, 0);
     return any != 0;
   };
@@ -253,11 +304,9 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
 
   if (warp < 4 * TILES) {
     // ---------------- softmax: one query row per thread ----------------
-    if constexpr (TILES == 2)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int tile = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_s = tmem + T::kScoreCol + 128 * tile + t_lane;
+    const uint32_t t_scores = tmem + T::kScoreCol + 2 * kChunk * tile + t_lane;
     const uint32_t t_o = tmem + T::kOutCol + D * tile + t_lane;
     const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
     if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta].last = -1;
@@ -325,11 +374,12 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       int page = page_of(k.c0);
 #pragma unroll 1
       for (int j = 0; j < chunks; ++j) {
-        const int p = (k.c0 + j) * kChunk;
+        const int p = (k.c0 + j) * kChunk, i0 = n + j;
+        const uint32_t t_s = t_scores + kChunk * (i0 & 1);
         // which 16-position groups of the chunk have a page
         const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0 && page < a.c.pages);
         page = page_of(k.c0 + j + 1);
-        ok = mbar_wait(s_full(tile), (n + j) & 1, gave_up);
+        ok = mbar_wait(s_full(tile, i0 & 1), (i0 >> 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         const bool plain = p + kChunk <= plain_end && pages == 0xffffffffu;
@@ -365,21 +415,18 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           tc_wait_store();
         }
-        // ---- the chunk's maximum; its first 64 scores stay in registers
+        // ---- the chunk's maximum
         uint32_t v[64];
+        tc_load32_async(t_s, v);
+        tc_load32_async(t_s + 32, v + 32);
+        tc_wait_load(v);
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          tc_load32_async(t_s + 64 * h, v);
-          tc_load32_async(t_s + 64 * h + 32, v + 32);
-          tc_wait_load(v);
+        for (int i = 0; i < 64; i += 8)
 #pragma unroll
-          for (int i = 0; i < 64; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx4[e] =
-                  fmaxf(fmaxf(mx4[e], __uint_as_float(v[i + 2 * e])), __uint_as_float(v[i + 2 * e + 1]));
-        }
+          for (int e = 0; e < 4; ++e)
+            mx4[e] =
+                fmaxf(fmaxf(mx4[e], __uint_as_float(v[i + 2 * e])), __uint_as_float(v[i + 2 * e + 1]));
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const bool grew = mx > lim;
         if (__any_sync(0xffffffffu, grew)) {
@@ -394,7 +441,10 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           __syncwarp();
           if (j > 0) {
-            // (the scores are done, so the products into the outputs issued before them are too)
+            // after the outputs of the chunk before
+            ok = mbar_wait(o_done(tile, (i0 - 1) & 1), ((i0 - 1) >> 1) & 1, gave_up);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t x[16];
@@ -406,7 +456,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
         }
         __syncwarp();
-        // ---- weights: f16 pairs over the scores, whose second 64 are read again
+        // ---- weights: f16 pairs over the scores
         auto weights = [&](int c, const uint32_t* x) {
           uint32_t w[16];
 #pragma unroll
@@ -420,20 +470,16 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           tc_store16(t_s + 16 * c, w);
         };
         weights(0, v);
-        tc_load32_async(t_s + 64, v);
         weights(1, v + 32);
-        tc_wait_load(v);
-        tc_load32_async(t_s + 96, v + 32);
-        weights(2, v);
-        tc_wait_load(v);
-        weights(3, v + 32);
         tc_wait_store();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(tile));
+        if (lane == 0) mbar_arrive(p_full(tile, i0 & 1));
       }
       if (!ok) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(o_full(tile), piece & 1, gave_up))) break;
+      const int last = n + chunks - 1;
+      ok = mbar_wait(o_done(tile, last & 1), (last >> 1) & 1, gave_up);
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const float sum = l.x + l.y;
       const bool whole = walk.whole();
@@ -482,71 +528,55 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       more = next_piece();
     }
   } else {
-    if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const int log_block = a.c.log_block, log_sb = log2_of(D) - log_block;
     PieceOf k;
-    // Lane i < 8 gets the place of the chunk's positions 16 i ..: the row of the cache (slots of one
-    // head) divided by 16, or -1.
-    auto page_rows = [&](int chunk) {
-      const int p = chunk * kChunk + 16 * lane;
-      int row = -1;
-      if (lane < kChunk / 16 && p < k.end) {
-        const int64_t slot = a.table.slot(a.c, k.b, p);
-        if (slot >= 0) row = (int)((slot + ((int64_t)k.h << a.c.page_shift)) >> 4);
-      }
-      return row;
-    };
     if (warp < 4 * TILES + kValueWarps) {
     // ---------------- values: 8 positions x D / 8 values per thread ----------------
     const int w4 = warp - 4 * TILES;
-    const int oct = lane & 7, half = w4 & 1;             // positions 64 half + 8 oct ..
-    const int run = (lane >> 3) + 4 * (w4 >> 1);         // values (D / 8) run ..
+    const int turn = w4 >> 1;                            // these two warps take every other chunk
+    const int oct = lane & 7;                            // positions 8 oct ..
+    const int run = (lane >> 3) + 4 * (w4 & 1);          // values (D / 8) run ..
     constexpr int W = D / 64;                            // code words per position
-    const uint8_t* src0 = a.c.codes[1] + (oct & 1) * (8 * (D / 2)) + (D / 16) * run;
-    const uint8_t* ss0 = a.c.scales[1] + ((8 * (oct & 1)) << log_sb) + (((D / 8) * run) >> log_block);
+    const uint32_t src = s_raw + T::kRawV + oct * T::kOctet + (D / 16) * run;
+    const uint32_t src_s = s_raw + T::kRawVS + ((8 * oct) << log_sb) + (((D / 8) * run) >> log_block);
     while (more) {
       k = PieceOf(walk);
       const int chunks = k.chunks;
-      uint32_t code[8][W], sc[8];
-      int rows = page_rows(k.c0);
-      auto load = [&](int j) {
-        const int p = (k.c0 + j) * kChunk + 64 * half + 8 * oct;
-        const int row = __shfl_sync(0xffffffffu, rows, 4 * half + (oct >> 1));
-        const int have = row >= 0 ? k.end - p : 0;       // positions from p on
-        const uint8_t* src = src0 + (uint64_t)(uint32_t)max(row, 0) * (16 * (D / 2));
-        const uint8_t* ss = ss0 + ((uint64_t)(uint32_t)max(row, 0) << (4 + log_sb));
-        rows = page_rows(k.c0 + j + 1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sc[i] = 0;
-#pragma unroll
-          for (int e = 0; e < W; ++e) code[i][e] = 0;
-          if (i < have) {
-            const uint8_t* at = src + i * (D / 2);
-            if constexpr (W == 1) code[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-            if constexpr (W == 2) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-              code[i][0] = v.x, code[i][1] = v.y;
-            }
-            if constexpr (W == 4) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
-              code[i][0] = v.x, code[i][1] = v.y, code[i][2] = v.z, code[i][3] = v.w;
-            }
-            const uint8_t* sp = ss + (i << log_sb);
-            if (W == 4 && log_block == 4) sc[i] = __ldg(reinterpret_cast<const uint16_t*>(sp));
-            else sc[i] = W == 4 ? __ldg(sp) * 0x101u : __ldg(sp);
-          }
-        }
-      };
-      load(0);
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < chunks; ++j) {
-        const int i = n + j, s = i % S;
-        if (i >= S) ok = mbar_wait<40>(v_empty(s), ((i / S) + 1) & 1, gave_up);
+        // every chunk's codes are waited for, also the other warps': a place of the ring that came round
+        // twice unseen could not be told from one that did not
+        const int i = n + j, s = i % S, r = i % R;
+        const bool ours = (i & 1) == turn;
+        ok = mbar_wait<20>(raw_full(r), (i / R) & 1, gave_up);
+        if (ok && ours && i >= S) ok = mbar_wait<20>(v_empty(s), ((i / S) + 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        // row d of the transposed tile: 128 bytes = this half's 64 positions
-        const uint32_t dst = s_v + s * T::kK + half * (D * 128);
+        if (!ours) {
+          if (lane == 0) mbar_arrive(raw_empty(r));
+          continue;
+        }
+        // positions from the thread's first one on that are there; zeros for the others (what else is in
+        // the ring may be NaN scales)
+        const int have = (s_pages[r] >> (oct >> 1)) & 1 ? k.end - (k.c0 + j) * kChunk - 8 * oct : 0;
+        uint32_t code[8][W], sc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lds<4 * W>(src + r * T::kRaw + e * (D / 2), code[e]);
+          const uint32_t at = src_s + r * T::kRaw + (e << log_sb);
+          sc[e] = W == 4 && log_block == 4 ? lds_u16(at) : lds_u8(at) * (W == 4 ? 0x101u : 1u);
+        }
+        if (have < 8) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e >= have) {
+              sc[e] = 0;
+#pragma unroll
+              for (int w = 0; w < W; ++w) code[e][w] = 0;
+            }
+        }
+        // row d of the transposed tile: 128 bytes = the chunk's 64 positions
+        const uint32_t dst = s_v + s * T::kK;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           uint32_t ev[4][4], od[4][4];  // [pair of positions][even / odd values 2 i, 2 i + 1]
@@ -576,116 +606,152 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(s));
-        if (j + 1 < chunks) load(j + 1);
+        if (lane == 0) {
+          mbar_arrive(v_full(s));
+          mbar_arrive(raw_empty(r));  // (every lane has used what it read)
+        }
       }
       if (!ok) break;
       n += chunks;
       more = next_piece();
     }
     } else if (warp < 4 * TILES + kValueWarps + kKeyWarps) {
-    // ---------------- keys: blocks of 32 positions x 32 values, one position per lane ----------------
-    const int w3 = warp - 4 * TILES - kValueWarps;
-    constexpr int kBlocks = D / 8;
+    // ---------------- keys: one position per thread ----------------
+    const int pos = 32 * (warp - 4 * TILES - kValueWarps) + lane;
+    const uint32_t src = s_raw + pos * (D / 2), src_s = s_raw + T::kRawKS + (pos << log_sb);
+    const uint32_t dst = s_k + (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
     while (more) {
       k = PieceOf(walk);
       const int chunks = k.chunks;
-      int rows = page_rows(k.c0), rows_next = page_rows(k.c0 + 1);
-      struct Block { uint4 code; uint32_t sc; };
-      // the place of a block: chunk lj, block lb; loads run two blocks ahead of the conversions
-      int lj = 0, lb = w3;
-      auto load = [&](Block& x) {
-        x.code = make_uint4(0, 0, 0, 0);
-        x.sc = 0;
-        if (lj >= chunks) return;
-        const int quarter = lb & 3, piece = lb >> 2;
-        const int row = __shfl_sync(0xffffffffu, rows, 2 * quarter + (lane >> 4));
-        if (row >= 0 && (k.c0 + lj) * kChunk + 32 * quarter + lane < k.end) {
-          const uint64_t at = (uint64_t)row * 16 + (lane & 15);
-          x.code = __ldg(reinterpret_cast<const uint4*>(a.c.codes[0] + at * (D / 2)) + piece);
-          const uint8_t* sp = a.c.scales[0] + (at << log_sb) + ((32 * piece) >> log_block);
-          if (log_block == 4) x.sc = __ldg(reinterpret_cast<const uint16_t*>(sp));
-          else x.sc = __ldg(sp) * 0x101u;
-        }
-        __syncwarp();
-        lb += kKeyWarps;
-        if (lb >= kBlocks) {
-          lb = w3;
-          ++lj;
-          rows = rows_next;
-          rows_next = page_rows(k.c0 + lj + 1);
-        }
-      };
-      Block x0, x1, x2;
-      load(x0);
-      load(x1);
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < chunks; ++j) {
-        const int i = n + j, s = i % S;
-        if (i >= S) ok = mbar_wait<40>(k_empty(s), ((i / S) + 1) & 1, gave_up);
+        const int i = n + j, s = i % S, r = i % R;
+        ok = mbar_wait<20>(raw_full(r), (i / R) & 1, gave_up);
+        if (ok && i >= S) ok = mbar_wait<20>(k_empty(s), ((i / S) + 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-#pragma unroll 1
-        for (int blk = w3; blk < kBlocks; blk += kKeyWarps) {
-          load(x2);
-          const int piece = blk >> 2, pos = 32 * (blk & 3) + lane;
-          const uint32_t dst = s_k + s * T::kK + (uint32_t)(piece >> 1) * 16384u +
-                               (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
-          const uint32_t w[4] = {x0.code.x, x0.code.y, x0.code.z, x0.code.w};
-          const uint32_t f2 = scale_pair<FMT>(x0.sc & 0xFFu, x0.sc >> 8);
+        const bool has = ((s_pages[r] >> (pos >> 4)) & 1) && (k.c0 + j) * kChunk + pos < k.end;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          // 32 values; lanes start at different ones, so that they read different banks
+          const uint32_t piece = (q + (lane >> 1)) & (D / 32 - 1);
+          uint32_t w[4];
+          lds<16>(src + r * T::kRaw + 16 * piece, w);
+          const uint32_t at = src_s + r * T::kRaw + ((32 * piece) >> log_block);
+          uint32_t b = log_block == 4 ? lds_u16(at) : lds_u8(at) * 0x101u;
+          if (!has) b = w[0] = w[1] = w[2] = w[3] = 0;
+          const uint32_t f2 = scale_pair<FMT>(b & 0xFFu, b >> 8);
           const uint32_t f[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
+          const uint32_t to = dst + s * T::kK + (piece >> 1) * (kChunk * 128u);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t x[4];
-            e2m1x8_to_f16(w[e], x);
-            st_shared16(dst + (((uint32_t)(4 * (piece & 1) + e) ^ (pos & 7u)) << 4),
-                        mul_f16x2(x[0], f[e >> 1]), mul_f16x2(x[1], f[e >> 1]),
-                        mul_f16x2(x[2], f[e >> 1]), mul_f16x2(x[3], f[e >> 1]));
+            uint32_t h[4];
+            e2m1x8_to_f16(w[e], h);
+            st_shared16(to + (((4 * (piece & 1) + e) ^ (pos & 7u)) << 4), mul_f16x2(h[0], f[e >> 1]),
+                        mul_f16x2(h[1], f[e >> 1]), mul_f16x2(h[2], f[e >> 1]),
+                        mul_f16x2(h[3], f[e >> 1]));
           }
-          x0 = x1;
-          x1 = x2;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(s));
+        if (lane == 0) {
+          mbar_arrive(k_full(s));
+          mbar_arrive(raw_empty(r));
+        }
       }
       if (!ok) break;
       n += chunks;
       more = next_piece();
     }
+    } else if (warp < 4 * TILES + kValueWarps + kKeyWarps + 1) {
+    // ---------------- copies of codes and scales: one per lane ----------------
+    // lanes 0..3: 16 positions' key codes, 4..7: their scales, 8..11: the values' scales, 12..19: 8
+    // positions' value codes
+    const int what = lane < 4 ? 0 : lane < 8 ? 1 : lane < 12 ? 2 : 3;
+    const int part = lane < 12 ? lane & 3 : lane - 12, sixteen = lane < 12 ? part : (part >> 1) & 3;
+    const int bytes = what == 0 ? 16 * (D / 2) : what == 3 ? 8 * (D / 2) : 16 << log_sb;
+    const uint8_t* base = what == 0   ? a.c.codes[0]
+                          : what == 1 ? a.c.scales[0]
+                          : what == 2 ? a.c.scales[1]
+                                      : a.c.codes[1] + (part & 1) * (8 * (D / 2));
+    const int pitch = what == 0 || what == 3 ? 16 * (D / 2) : 16 << log_sb;  // of 16 positions
+    const uint32_t dst = s_raw + (what == 0   ? part * bytes
+                                  : what == 1 ? T::kRawKS + part * bytes
+                                  : what == 2 ? T::kRawVS + part * bytes
+                                              : T::kRawV + part * T::kOctet);
+    // the place of this lane's 16 positions of a chunk: the row of the cache (slots of one head) divided
+    // by 16, or -1
+    auto place = [&](int chunk) {
+      const int p = chunk * kChunk + 16 * sixteen;
+      int row = -1;
+      if (lane < 20 && p < k.end) {
+        const int64_t slot = a.table.slot(a.c, k.b, p);
+        if (slot >= 0) row = (int)((slot + ((int64_t)k.h << a.c.page_shift)) >> 4);
+      }
+      return row;
+    };
+    int issued = 0;
+    while (more) {
+      k = PieceOf(walk);
+      const int chunks = k.chunks;
+      bool ok = true;
+      int row = place(k.c0);
+#pragma unroll 1
+      for (int j = 0; j < chunks; ++j) {
+        const int i = n + j, r = i % R;
+        const int here = row;
+        row = place(k.c0 + j + 1);
+        if (i >= R) ok = mbar_wait<20>(raw_empty(r), ((i / R) + 1) & 1, gave_up);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const uint32_t pages = __ballot_sync(0xffffffffu, here >= 0) & 15u;
+        if (lane == 0) {
+          s_pages[r] = pages;
+          mbar_arrive_expect_tx(raw_full(r), __popc(pages) * (2 * 16 * (D / 2) + 2 * (16 << log_sb)));
+        }
+        __syncwarp();
+        if (here >= 0)
+          bulk_copy(dst + r * T::kRaw, base + (uint64_t)(uint32_t)here * pitch, bytes, raw_full(r));
+        issued = i + 1;
+      }
+      if (!ok) break;
+      n += chunks;
+      more = next_piece();
+    }
+    if (*gave_up) {  // copies in flight end before the block does
+      for (int i = max(0, issued - R); i < issued; ++i) {
+        int unused = 0;
+        mbar_wait(raw_full(i % R), (i / R) & 1, &unused);
+      }
+    }
+    __syncwarp();
     } else {
     // ---------------- products (one elected thread; the warp stays together) ----------------
       const bool one = elect_one();
-      auto scores = [&](int t, int s) {
+      auto scores = [&](int t, int i) {  // of chunk i
         if (one) {
-          uint64_t qd = desc_sw128(s_q + t * T::kQ), kd = desc_sw128(s_k + s * T::kK);
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {  // 64 values of the head: 16 KB apart, 32 bytes per step
+          const int s = i % S, buf = i & 1;
+          const uint32_t qd = desc_low(s_q + t * T::kQ), kd = desc_low(s_k + s * T::kK);
+          const uint32_t d = tmem + T::kScoreCol + kChunk * (2 * t + buf);
+          // 16 values of the head a step: 32 bytes on, after 64 the next 128-byte-wide block
+          mma_ss<false>(d, qd, kd, T::kIdescS);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              tc_mma_f16(tmem + T::kScoreCol + 128 * t, qd + 2 * x, kd + 2 * x, T::kIdescS,
-                         c > 0 || x > 0);
-            qd += 16384 >> 4;
-            kd += 16384 >> 4;
-          }
-          tc_commit(s_full(t));
+          for (int x = 1; x < D / 16; ++x)
+            mma_ss<true>(d, qd + (x >> 2) * ((128 * 128) >> 4) + 2 * (x & 3),
+                         kd + (x >> 2) * ((kChunk * 128) >> 4) + 2 * (x & 3), T::kIdescS);
+          tc_commit(s_full(t, buf));
           if (t == TILES - 1) tc_commit(k_empty(s));
         }
         __syncwarp();
       };
-      auto outputs = [&](int t, int s, bool add) {
+      auto outputs = [&](int t, int i, bool add) {
         if (one) {
-          uint64_t vd = desc_sw128(s_v + s * T::kK);
-          uint32_t pa = tmem + T::kScoreCol + 128 * t;
-#pragma unroll 1
-          for (int c = 0; c < kChunk / 64; ++c) {  // 64 positions
+          const int s = i % S, buf = i & 1;
+          const uint32_t vd = desc_low(s_v + s * T::kK);
+          const uint32_t pa = tmem + T::kScoreCol + kChunk * (2 * t + buf);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              tc_mma_f16_ts(tmem + T::kOutCol + D * t, pa + 8 * x, vd + 2 * x, T::kIdescO,
-                            add || c > 0 || x > 0);
-            pa += 32;
-            vd += (D * 128) >> 4;
-          }
+          for (int x = 0; x < kChunk / 16; ++x)
+            mma_ts(tmem + T::kOutCol + D * t, pa + 8 * x, vd + 2 * x, T::kIdescO, add || x > 0);
+          tc_commit(o_done(t, buf));
           if (t == TILES - 1) tc_commit(v_empty(s));
         }
         __syncwarp();
@@ -700,25 +766,22 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         ok = ok && wait(k_full(n % S), (n / S) & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < TILES; ++t) scores(t, n % S);
+        for (int t = 0; t < TILES; ++t) scores(t, n);
 #pragma unroll 1
         for (int j = 0; j < chunks && ok; ++j) {
           const int i = n + j, s = i % S;
-#pragma unroll 1
+#pragma unroll
           for (int t = 0; t < TILES; ++t) {
-            ok = wait(p_full(t), i & 1);
-            if (ok && t == 0) ok = wait(v_full(s), (i / S) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            outputs(t, s, j > 0);
+            // into the buffer whose weights the outputs issued before this have read
             if (j + 1 < chunks) {
               if (t == 0) ok = wait(k_full((i + 1) % S), ((i + 1) / S) & 1);
-              if (!ok) break;
               tc_fence_after();
-              scores(t, (i + 1) % S);
-            } else if (one) {
-              tc_commit(o_full(t));
+              if (ok) scores(t, i + 1);
             }
+            if (ok) ok = wait(p_full(t, i & 1), (i >> 1) & 1);
+            if (ok && t == 0) ok = wait(v_full(s), (i / S) & 1);
+            tc_fence_after();
+            if (ok) outputs(t, i, j > 0);
           }
         }
         n += chunks;
@@ -752,14 +815,6 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream, int* launches) {
   auto* kern = k_attention_tile<D, TILES, FMT>;
   cudaError_t e = allow_dynamic_smem(attr, kern, T::kSmem);
   if (e != cudaSuccess) return e;
-  if (TILES == 2) {
-    // the split of registers holds for this launch's count only
-    static const int regs = [&] {
-      cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  }
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
