@@ -725,71 +725,65 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     }
     __syncwarp();
     } else {
-    // ---------------- products (one elected thread; the warp stays together) ----------------
-      const bool one = elect_one();
-      auto scores = [&](int t, int i) {  // of chunk i
-        if (one) {
-          const int s = i % S, buf = i & 1;
-          const uint32_t qd = desc_low(s_q + t * T::kQ), kd = desc_low(s_k + s * T::kK);
-          const uint32_t d = tmem + T::kScoreCol + kChunk * (2 * t + buf);
-          // 16 values of the head a step: 32 bytes on, after 64 the next 128-byte-wide block
-          mma_ss<false>(d, qd, kd, T::kIdescS);
+    // ---------------- products (one elected thread) ----------------
+    if (more && elect_one()) {
+      auto scores = [&](int t, int i, int s) {  // of chunk i, its keys in stage s
+        const uint32_t qd = desc_low(s_q + t * T::kQ), kd = desc_low(s_k + s * T::kK);
+        const uint32_t d = tmem + T::kScoreCol + kChunk * (2 * t + (i & 1));
+        // 16 values of the head a step: 32 bytes on, after 64 the next 128-byte-wide block
+        mma_ss<false>(d, qd, kd, T::kIdescS);
 #pragma unroll
-          for (int x = 1; x < D / 16; ++x)
-            mma_ss<true>(d, qd + (x >> 2) * ((128 * 128) >> 4) + 2 * (x & 3),
-                         kd + (x >> 2) * ((kChunk * 128) >> 4) + 2 * (x & 3), T::kIdescS);
-          tc_commit(s_full(t, buf));
-          if (t == TILES - 1) tc_commit(k_empty(s));
-        }
-        __syncwarp();
+        for (int x = 1; x < D / 16; ++x)
+          mma_ss<true>(d, qd + (x >> 2) * ((128 * 128) >> 4) + 2 * (x & 3),
+                       kd + (x >> 2) * ((kChunk * 128) >> 4) + 2 * (x & 3), T::kIdescS);
+        tc_commit(s_full(t, i & 1));
+        if (t == TILES - 1) tc_commit(k_empty(s));
       };
-      auto outputs = [&](int t, int i, bool add) {
-        if (one) {
-          const int s = i % S, buf = i & 1;
-          const uint32_t vd = desc_low(s_v + s * T::kK);
-          const uint32_t pa = tmem + T::kScoreCol + kChunk * (2 * t + buf);
+      auto outputs = [&](int t, int i, int s, bool add) {
+        const uint32_t vd = desc_low(s_v + s * T::kK);
+        const uint32_t pa = tmem + T::kScoreCol + kChunk * (2 * t + (i & 1));
+        mma_ts(tmem + T::kOutCol + D * t, pa, vd, T::kIdescO, add);
 #pragma unroll
-          for (int x = 0; x < kChunk / 16; ++x)
-            mma_ts(tmem + T::kOutCol + D * t, pa + 8 * x, vd + 2 * x, T::kIdescO, add || x > 0);
-          tc_commit(o_done(t, buf));
-          if (t == TILES - 1) tc_commit(v_empty(s));
-        }
-        __syncwarp();
-      };
-      auto wait = [&](uint32_t b, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(b, parity, gave_up));
+        for (int x = 1; x < kChunk / 16; ++x)
+          mma_ts(tmem + T::kOutCol + D * t, pa + 8 * x, vd + 2 * x, T::kIdescO, true);
+        tc_commit(o_done(t, i & 1));
+        if (t == TILES - 1) tc_commit(v_empty(s));
       };
       bool ok = true;
-      while (more && ok) {
+      while (ok) {
         const int chunks = walk.c1 - walk.c0;
-        for (int t = 0; t < TILES && ok; ++t) ok = wait(q_full(t), piece & 1);
-        ok = ok && wait(k_full(n % S), (n / S) & 1);
+        for (int t = 0; t < TILES && ok; ++t) ok = mbar_wait(q_full(t), piece & 1, gave_up);
+        ok = ok && mbar_wait(k_full(n % S), (n / S) & 1, gave_up);
         if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < TILES; ++t) scores(t, n);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) scores(t, n, n % S);
+        const int stop = n + chunks;
 #pragma unroll 1
-        for (int j = 0; j < chunks && ok; ++j) {
-          const int i = n + j, s = i % S;
+        for (; n < stop; ++n) {
+          const int s = n % S, s1 = (n + 1) % S;
+          const bool go = n + 1 < stop;
+          if (go && !(ok = mbar_wait(k_full(s1), ((n + 1) / S) & 1, gave_up))) break;
+          if (!(ok = mbar_wait(v_full(s), (n / S) & 1, gave_up))) break;
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
-            // into the buffer whose weights the outputs issued before this have read
-            if (j + 1 < chunks) {
-              if (t == 0) ok = wait(k_full((i + 1) % S), ((i + 1) / S) & 1);
-              tc_fence_after();
-              if (ok) scores(t, i + 1);
-            }
-            if (ok) ok = wait(p_full(t, i & 1), (i >> 1) & 1);
-            if (ok && t == 0) ok = wait(v_full(s), (i / S) & 1);
             tc_fence_after();
-            if (ok) outputs(t, i, j > 0);
+            // into the buffer whose weights the outputs issued before this have read
+            if (go) scores(t, n + 1, s1);
+            if (!(ok = mbar_wait(p_full(t, n & 1), (n >> 1) & 1, gave_up))) break;
+            tc_fence_after();
+            outputs(t, n, s, n > stop - chunks);
           }
+          if (!ok) break;
         }
-        n += chunks;
         ++piece;
-        more = next_piece();
+        if (!ok || !walk.next(a, cut)) break;
       }
-      if (one) tc_commit(done);  // also after giving up: every issued product
-      __syncwarp();
+      tc_commit(done);  // also after giving up: every issued product
+    } else if (!more && lane == 0) {
+      tc_commit(done);
+    }
+    __syncwarp();
     }
   }
 
