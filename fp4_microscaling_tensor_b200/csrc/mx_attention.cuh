@@ -220,6 +220,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 16 bytes into shared memory; of the form with a size, the rest are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int BYTES>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t* v) {
   if constexpr (BYTES == 16)

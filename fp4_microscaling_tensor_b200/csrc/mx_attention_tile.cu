@@ -3,7 +3,7 @@
 //
 // The formulas are those of mx_cache_attention.cu.  With 128 query rows and more per key/value head the
 // products dominate: 4 D multiply-adds per row and position against 1 + 2 / N bytes per position and
-// dimension.  So K and V are dequantized once per chunk of 64 positions into shared memory (f16,
+// dimension.  So K and V are dequantized once per chunk of 128 positions into shared memory (f16,
 // exact) and serve TILES x 128 rows; scores and outputs stay in tensor memory.
 //
 // One thread block per SM, whose warps have one job each:
@@ -11,19 +11,20 @@
 //     then per chunk, one row per thread: read the scores from tensor memory, mask, weights
 //     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
 //     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
-//   * 1 warp: brings the chunks' codes and scales into a ring in shared memory (bulk copies), up to
-//     three chunks ahead;
+//   * 1 warp: brings codes and scales into a ring in shared memory (16-byte asynchronous copies; bulk
+//     copies of the 64- to 1024-byte runs that a page holds took 1.4 times as long in all);
 //   * 2 warps: a chunk's keys, one position per thread, into the K-major B operand of q K^T;
-//   * 4 warps: its values (two of them every other chunk), 8 positions x D / 8 values per thread,
+//   * 4 warps: its values (two of them every other half), 8 positions x D / 8 values per thread,
 //     transposed into the K-major (along the positions) B operand of p V: two positions' codes are
 //     interleaved as nibbles, so that a conversion gives f16 pairs along the positions and no data moves
 //     between threads;
-//   * 1 warp, one thread: issues the products: a tile's scores of the next chunk before its outputs of
-//     this one, so that its softmax warps always have scores to go on with.  p comes from tensor memory
-//     (A operand).
-// Tensor memory per tile: two buffers of 64 columns of scores (weights overlay them), D columns of
-// outputs.  (Chunks of 128 positions with one buffer per tile left the softmax waiting for its own
-// products: 1158 us for 2048 prompt tokens over 16384 positions, 64 heads on 8, against 0.)
+//   * 1 warp, one thread: issues the products.  Two tiles take turns: while one tile's weights are
+//     computed, the tensor cores work on the other's.  p comes from tensor memory (A operand), half a
+//     chunk at a time.
+// Keys, values and codes move in halves of a chunk.  Tensor memory per tile: 128 columns of scores
+// (weights overlay them), D columns of outputs.  (Two buffers of 64 columns would let a tile's scores run
+// ahead of its weights, but products 64 columns wide take as long as those 128 wide: measured 1198 us
+// for 2048 prompt tokens over 16384 positions, 64 heads on 8, against @@ us.)
 //
 // Every wait is bounded (mbar_wait below): a block that gives up says so in a device counter
 // (mx_matmul_gave_up), lets its issued products finish, frees its tensor memory and returns; blocks do
@@ -41,8 +42,8 @@ __device__ unsigned int g_tile_gave_up;
 
 namespace {
 
-constexpr int kChunk = 64;  // positions per chunk
-constexpr int kTileStart = 4;  // Cut::start, in chunks
+constexpr int kChunk = 128, kHalf = 64;  // positions per chunk, and per step of its loads
+constexpr int kTileStart = 2;  // Cut::start, in chunks
 constexpr int kKeyWarps = 2, kValueWarps = 4;
 constexpr uint32_t kPolls = 1u << 20;
 constexpr float kSlack = 8.0f;
@@ -50,19 +51,19 @@ constexpr float kSlack = 8.0f;
 template <int D, int TILES>
 struct Tile {
   static constexpr int kRows = 128 * TILES;
-  static constexpr int kStages = D == 256 ? 2 : 4;
+  static constexpr int kStages = D == 256 ? 2 : 4;       // of half a chunk
   static constexpr int kQ = 128 * D * 2;                // bytes of one tile's queries
-  static constexpr int kK = kChunk * D * 2;             // bytes of a chunk's keys (and values)
+  static constexpr int kK = kHalf * D * 2;              // bytes of half a chunk's keys (and values)
   // ring of codes and scales: keys, values (8 positions at a time, 16 bytes apart, so that the threads
   // of 8 runs of 8 positions read different banks), their scales (at most one per 16 values)
   static constexpr int kRing = D == 256 ? 1 : 3;
   static constexpr int kOctet = 8 * (D / 2) + 16;
-  static constexpr int kRawV = kChunk * (D / 2), kRawKS = kRawV + kChunk / 8 * kOctet,
-                       kRawVS = kRawKS + kChunk * (D / 16), kRaw = kRawVS + kChunk * (D / 16);
+  static constexpr int kRawV = kHalf * (D / 2), kRawKS = kRawV + kHalf / 8 * kOctet,
+                       kRawVS = kRawKS + kHalf * (D / 16), kRaw = kRawVS + kHalf * (D / 16);
   static constexpr int kSmem = TILES * kQ + 2 * kStages * kK + kRing * kRaw + 1024;
   static_assert(kSmem <= 230000, "shared memory");
   static constexpr int kThreads = 128 * (TILES + 2);
-  static constexpr uint32_t kScoreCol = 0, kOutCol = 2 * kChunk * TILES;
+  static constexpr uint32_t kScoreCol = 0, kOutCol = kChunk * TILES;
   static_assert(kOutCol + TILES * D <= 512, "tensor memory");
   // Instruction descriptors of kind::f16: float32 accumulator (bits 4..5 = 1), A and B f16, K-major,
   // N / 8 in bits 17..22, M / 16 in bits 24..28.
@@ -90,19 +91,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
   *gave_up = 1;
   return false;
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
 }
 
 // True in one lane of the warp, which is converged.
@@ -215,8 +203,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   const uint32_t s_q = smem_u32(smem), s_k = s_q + TILES * T::kQ, s_v = s_k + S * T::kK,
                  s_raw = s_v + S * T::kK;
   constexpr int R = T::kRing;
-  __shared__ uint64_t bars[14 + 4 * S + 2 * R + 1];
-  __shared__ uint32_t s_pages[R];  // which 16 positions of the ring's chunks have a page
+  __shared__ uint64_t bars[10 + 4 * S + 2 * R + 1];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_gave_up;
   __shared__ int64_t s_scan[T::kThreads / 32];
@@ -224,42 +211,39 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   __shared__ Walk s_walk[T::kThreads / 32];
   volatile int* gave_up = &s_gave_up;
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  // barriers: per tile, queries in place, and for every other chunk, scores done, weights in place,
-  // outputs done; per stage, keys and values in place and read; per place of the ring, codes in place and
-  // read.  (A wait by parity is sound where the
-  // phase before the awaited one is known to be over and the one behind it cannot end before the wait
-  // does; softmax and products may be two chunks apart, so the chunks' barriers come in pairs.)
+  // barriers: per tile, queries in place, scores done, weights in place (by halves), outputs done; per
+  // stage (a chunk), keys in place, keys and values read, per half of it, values in place; per place of
+  // the ring, codes in place and read.  (A wait by parity is sound where the phase before the awaited one
+  // is known to be over, and the one behind it cannot end before the wait does.)
   auto q_full = [&](int t) { return bar(t); };
-  auto o_done = [&](int t, int buf) { return bar(2 + 2 * t + buf); };
-  auto s_full = [&](int t, int buf) { return bar(6 + 2 * t + buf); };
-  auto p_full = [&](int t, int buf) { return bar(10 + 2 * t + buf); };
-  auto k_full = [&](int s) { return bar(14 + s); };
-  auto k_empty = [&](int s) { return bar(14 + S + s); };
-  auto v_full = [&](int s) { return bar(14 + 2 * S + s); };
-  auto v_empty = [&](int s) { return bar(14 + 3 * S + s); };
-  auto raw_full = [&](int r) { return bar(14 + 4 * S + r); };
-  auto raw_empty = [&](int r) { return bar(14 + 4 * S + R + r); };
-  const uint32_t done = bar(14 + 4 * S + 2 * R);
+  auto o_full = [&](int t) { return bar(2 + t); };
+  auto s_full = [&](int t) { return bar(4 + t); };
+  auto p_full = [&](int t, int half) { return bar(6 + 2 * t + half); };
+  auto k_full = [&](int s) { return bar(10 + s); };
+  auto k_empty = [&](int s) { return bar(10 + S + s); };
+  auto v_empty = [&](int s) { return bar(10 + 2 * S + s); };
+  auto v_full = [&](int half) { return bar(10 + 3 * S + half); };
+  auto raw_full = [&](int r) { return bar(10 + 4 * S + r); };
+  auto raw_empty = [&](int r) { return bar(10 + 4 * S + R + r); };
+  const uint32_t done = bar(10 + 4 * S + 2 * R);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.heads / a.c.kv_heads, ctas = gridDim.x, cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 4);
-      for (int buf = 0; buf < 2; ++buf) {
-        mbar_init(o_done(t, buf), 1);
-        mbar_init(s_full(t, buf), 1);
-        mbar_init(p_full(t, buf), 4);
-      }
+      mbar_init(o_full(t), 1);
+      mbar_init(s_full(t), 1);
+      for (int half = 0; half < 2; ++half) mbar_init(p_full(t, half), 4);
     }
     for (int s = 0; s < S; ++s) {
-      mbar_init(k_full(s), kKeyWarps);
+      mbar_init(k_full(s), 2 * kKeyWarps);  // (by halves)
       mbar_init(k_empty(s), 1);
       mbar_init(v_full(s), kValueWarps / 2);
       mbar_init(v_empty(s), 1);
     }
     for (int r = 0; r < R; ++r) {
-      mbar_init(raw_full(r), 1);
+      mbar_init(raw_full(r), 32);
       mbar_init(raw_empty(r), kKeyWarps + kValueWarps);
     }
     mbar_init(done, 1);
@@ -306,7 +290,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     // ---------------- softmax: one query row per thread ----------------
     const int tile = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_scores = tmem + T::kScoreCol + 2 * kChunk * tile + t_lane;
+    const uint32_t t_s = tmem + T::kScoreCol + kChunk * tile + t_lane;
     const uint32_t t_o = tmem + T::kOutCol + D * tile + t_lane;
     const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
     if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta].last = -1;
@@ -314,6 +298,10 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       const PieceOf k(walk);
       const Seq seq(a, k.b);
       const int rows = seq.count * group, row = k.rt * T::kRows + 128 * tile + r;
+      if (TILES > 1 && rows - k.rt * T::kRows <= 128 * tile) {  // no rows here (tile 0 always has some)
+        more = next_piece();
+        continue;
+      }
       const bool in = row < rows;
       const int t = in ? row / group : 0, head = k.h * group + (in ? row % group : 0);
       float mult;
@@ -364,43 +352,49 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       float m = -INFINITY, mu = 0.0f, lim = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);
       bool ok = true;
-      // the page number of this lane's 16 positions of a chunk (0 where it does not matter), loaded a
-      // chunk ahead: a wait for the table would be in the way of everything else
-      auto page_of = [&](int chunk) {
-        const int at = chunk * kChunk + 16 * lane;
-        return lane < kChunk / 16 && at < k.end
-                   ? __ldg(a.table.pages + k.b * a.table.stride + (at >> a.c.page_shift)) : 0;
-      };
-      int page = page_of(k.c0);
+      // whether any position of the piece has no page (then its chunks look them up again, below)
+      bool holes = false;
+      {
+        const int shift = a.c.page_shift;
+        const int32_t* ids = a.table.pages + k.b * a.table.stride;
+        const int stop = min(k.end, (k.c0 + chunks) * kChunk);
+        for (int g = ((k.c0 * kChunk) >> shift) + lane; g << shift < stop; g += 32) {
+          const int id = __ldg(ids + g);
+          holes |= id < 0 || id >= a.c.pages;
+        }
+        holes = __any_sync(0xffffffffu, holes);
+      }
+      // chunks before this one need no mask
+      const int plain = holes ? 0 : plain_end / kChunk - k.c0;
 #pragma unroll 1
       for (int j = 0; j < chunks; ++j) {
-        const int p = (k.c0 + j) * kChunk, i0 = n + j;
-        const uint32_t t_s = t_scores + kChunk * (i0 & 1);
-        // which 16-position groups of the chunk have a page
-        const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0 && page < a.c.pages);
-        page = page_of(k.c0 + j + 1);
-        ok = mbar_wait(s_full(tile, i0 & 1), (i0 >> 1) & 1, gave_up);
+        ok = mbar_wait(s_full(tile), (n + j) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        const bool plain = p + kChunk <= plain_end && pages == 0xffffffffu;
-        // bit i of seen(c): whether this row sees position p + 32 c + i
-        auto seen = [&](int c) -> uint32_t {
-          const int first = p + 32 * c;
-          auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u; };
-          uint32_t w = below(k.end - first);
-          if (a.tree) {
-            const int j0 = first - seq.base;  // the group's first position among the new tokens
-            const uint64_t have = seq.count >= 64 ? ~0ull : (1ull << seq.count) - 1ull;
-            const uint64_t v = word & have;
-            w &= j0 >= 64 ? 0u : j0 >= 0 ? (uint32_t)(v >> j0)
-                 : j0 <= -32 ? ~0u : ((uint32_t)(v << -j0) | below(-j0));
-          } else {
-            w &= below(seq.base + t + 1 - first);
-          }
-          return w & (((pages >> (2 * c)) & 1 ? 0xFFFFu : 0u) |
-                      ((pages >> (2 * c + 1)) & 1 ? 0xFFFF0000u : 0u));
-        };
-        if (!plain) {
+        if (j >= plain) {
+          const int p = (k.c0 + j) * kChunk;
+          // which 16-position groups of the chunk have a page
+          bool page = true;
+          if (holes && lane < kChunk / 16 && p + 16 * lane < k.end)
+            page = a.table.slot(a.c, k.b, p + 16 * lane) >= 0;
+          const uint32_t pages = __ballot_sync(0xffffffffu, page);
+          // bit i of seen(c): whether this row sees position p + 32 c + i
+          auto seen = [&](int c) -> uint32_t {
+            const int first = p + 32 * c;
+            auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u; };
+            uint32_t w = below(k.end - first);
+            if (a.tree) {
+              const int j0 = first - seq.base;  // the group's first position among the new tokens
+              const uint64_t have = seq.count >= 64 ? ~0ull : (1ull << seq.count) - 1ull;
+              const uint64_t v = word & have;
+              w &= j0 >= 64 ? 0u : j0 >= 0 ? (uint32_t)(v >> j0)
+                   : j0 <= -32 ? ~0u : ((uint32_t)(v << -j0) | below(-j0));
+            } else {
+              w &= below(seq.base + t + 1 - first);
+            }
+            return w & (((pages >> (2 * c)) & 1 ? 0xFFFFu : 0u) |
+                        ((pages >> (2 * c + 1)) & 1 ? 0xFFFF0000u : 0u));
+          };
           // boundary chunks (few): the scores that this row does not see become -infinity in place
 #pragma unroll 1
           for (int c = 0; c < kChunk / 16; ++c) {
@@ -415,18 +409,21 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           tc_wait_store();
         }
-        // ---- the chunk's maximum
+        // ---- the chunk's maximum; its first 64 scores stay in registers
         uint32_t v[64];
-        tc_load32_async(t_s, v);
-        tc_load32_async(t_s + 32, v + 32);
-        tc_wait_load(v);
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; i += 8)
+        for (int h = 1; h >= 0; --h) {
+          tc_load32_async(t_s + 64 * h, v);
+          tc_load32_async(t_s + 64 * h + 32, v + 32);
+          tc_wait_load(v);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx4[e] =
-                fmaxf(fmaxf(mx4[e], __uint_as_float(v[i + 2 * e])), __uint_as_float(v[i + 2 * e + 1]));
+          for (int i = 0; i < 64; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx4[e] =
+                  fmaxf(fmaxf(mx4[e], __uint_as_float(v[i + 2 * e])), __uint_as_float(v[i + 2 * e + 1]));
+        }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const bool grew = mx > lim;
         if (__any_sync(0xffffffffu, grew)) {
@@ -441,10 +438,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           __syncwarp();
           if (j > 0) {
-            // after the outputs of the chunk before
-            ok = mbar_wait(o_done(tile, (i0 - 1) & 1), ((i0 - 1) >> 1) & 1, gave_up);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            tc_fence_after();
+            // (the scores are done, so the products into the outputs issued before them are too)
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t x[16];
@@ -469,16 +463,25 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           tc_store16(t_s + 16 * c, w);
         };
+        auto in_place = [&](int half) {
+          tc_wait_store();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(tile, half));
+        };
         weights(0, v);
+        tc_load32_async(t_s + 64, v);
         weights(1, v + 32);
-        tc_wait_store();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(tile, i0 & 1));
+        tc_wait_load(v);
+        tc_load32_async(t_s + 96, v + 32);
+        in_place(0);
+        weights(2, v);
+        tc_wait_load(v);
+        weights(3, v + 32);
+        in_place(1);
       }
       if (!ok) break;
-      const int last = n + chunks - 1;
-      ok = mbar_wait(o_done(tile, last & 1), (last >> 1) & 1, gave_up);
+      ok = mbar_wait(o_full(tile), piece & 1, gave_up);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const float sum = l.x + l.y;
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     if (warp < 4 * TILES + kValueWarps) {
     // ---------------- values: 8 positions x D / 8 values per thread ----------------
     const int w4 = warp - 4 * TILES;
-    const int turn = w4 >> 1;                            // these two warps take every other chunk
+    const int turn = w4 >> 1;                            // these two warps take every other half
     const int oct = lane & 7;                            // positions 8 oct ..
     const int run = (lane >> 3) + 4 * (w4 & 1);          // values (D / 8) run ..
     constexpr int W = D / 64;                            // code words per position
@@ -541,24 +544,21 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     const uint32_t src_s = s_raw + T::kRawVS + ((8 * oct) << log_sb) + (((D / 8) * run) >> log_block);
     while (more) {
       k = PieceOf(walk);
-      const int chunks = k.chunks;
+      const int halves = 2 * k.chunks, h0 = 2 * k.c0;
       bool ok = true;
 #pragma unroll 1
-      for (int j = 0; j < chunks; ++j) {
-        // every chunk's codes are waited for, also the other warps': a place of the ring that came round
+      for (int j = 0; j < halves; ++j) {
+        // every half's codes are waited for, also the other warps': a place of the ring that came round
         // twice unseen could not be told from one that did not
         const int i = n + j, s = i % S, r = i % R;
         const bool ours = (i & 1) == turn;
         ok = mbar_wait<20>(raw_full(r), (i / R) & 1, gave_up);
-        if (ok && ours && i >= S) ok = mbar_wait<20>(v_empty(s), ((i / S) + 1) & 1, gave_up);
+        if (ok && ours && i >= S) ok = mbar_wait<20>(v_empty(s >> 1), ((i / S) + 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         if (!ours) {
           if (lane == 0) mbar_arrive(raw_empty(r));
           continue;
         }
-        // positions from the thread's first one on that are there; zeros for the others (what else is in
-        // the ring may be NaN scales)
-        const int have = (s_pages[r] >> (oct >> 1)) & 1 ? k.end - (k.c0 + j) * kChunk - 8 * oct : 0;
         uint32_t code[8][W], sc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -566,16 +566,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           const uint32_t at = src_s + r * T::kRaw + (e << log_sb);
           sc[e] = W == 4 && log_block == 4 ? lds_u16(at) : lds_u8(at) * (W == 4 ? 0x101u : 1u);
         }
-        if (have < 8) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e >= have) {
-              sc[e] = 0;
-#pragma unroll
-              for (int w = 0; w < W; ++w) code[e][w] = 0;
-            }
-        }
-        // row d of the transposed tile: 128 bytes = the chunk's 64 positions
+        // row d of the transposed tile: 128 bytes = 64 positions
         const uint32_t dst = s_v + s * T::kK;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
@@ -612,7 +603,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         }
       }
       if (!ok) break;
-      n += chunks;
+      n += halves;
       more = next_piece();
     }
     } else if (warp < 4 * TILES + kValueWarps + kKeyWarps) {
@@ -622,32 +613,35 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     const uint32_t dst = s_k + (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
     while (more) {
       k = PieceOf(walk);
-      const int chunks = k.chunks;
+      const int halves = 2 * k.chunks, h0 = 2 * k.c0;
       bool ok = true;
 #pragma unroll 1
-      for (int j = 0; j < chunks; ++j) {
+      for (int j = 0; j < halves; ++j) {
         const int i = n + j, s = i % S, r = i % R;
         ok = mbar_wait<20>(raw_full(r), (i / R) & 1, gave_up);
-        if (ok && i >= S) ok = mbar_wait<20>(k_empty(s), ((i / S) + 1) & 1, gave_up);
+        if (ok && i >= S) ok = mbar_wait<20>(k_empty(s >> 1), ((i / S) + 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const bool has = ((s_pages[r] >> (pos >> 4)) & 1) && (k.c0 + j) * kChunk + pos < k.end;
+        // runs of 32 values; lanes start at different ones, so that they read different banks
+        uint32_t w[D / 32][4], sc[D / 32];
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
-          // 32 values; lanes start at different ones, so that they read different banks
-          const uint32_t piece = (q + (lane >> 1)) & (D / 32 - 1);
-          uint32_t w[4];
-          lds<16>(src + r * T::kRaw + 16 * piece, w);
-          const uint32_t at = src_s + r * T::kRaw + ((32 * piece) >> log_block);
-          uint32_t b = log_block == 4 ? lds_u16(at) : lds_u8(at) * 0x101u;
-          if (!has) b = w[0] = w[1] = w[2] = w[3] = 0;
-          const uint32_t f2 = scale_pair<FMT>(b & 0xFFu, b >> 8);
+          const uint32_t run = (q + (lane >> 1)) & (D / 32 - 1);
+          lds<16>(src + r * T::kRaw + 16 * run, w[q]);
+          const uint32_t at = src_s + r * T::kRaw + ((32 * run) >> log_block);
+          sc[q] = log_block == 4 ? lds_u16(at) : lds_u8(at) * 0x101u;
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          const uint32_t run = (q + (lane >> 1)) & (D / 32 - 1);
+          const uint32_t f2 = scale_pair<FMT>(sc[q] & 0xFFu, sc[q] >> 8);
           const uint32_t f[2] = {__byte_perm(f2, f2, 0x1010), __byte_perm(f2, f2, 0x3232)};
-          const uint32_t to = dst + s * T::kK + (piece >> 1) * (kChunk * 128u);
+          const uint32_t to = dst + (s >> 1) * (2 * T::kK) + (s & 1) * (kHalf * 128u) +
+                              (run >> 1) * (kChunk * 128u);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t h[4];
-            e2m1x8_to_f16(w[e], h);
-            st_shared16(to + (((4 * (piece & 1) + e) ^ (pos & 7u)) << 4), mul_f16x2(h[0], f[e >> 1]),
+            e2m1x8_to_f16(w[q][e], h);
+            st_shared16(to + (((4 * (run & 1) + e) ^ (pos & 7u)) << 4), mul_f16x2(h[0], f[e >> 1]),
                         mul_f16x2(h[1], f[e >> 1]), mul_f16x2(h[2], f[e >> 1]),
                         mul_f16x2(h[3], f[e >> 1]));
           }
@@ -655,133 +649,163 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(k_full(s));
+          mbar_arrive(k_full(s >> 1));
           mbar_arrive(raw_empty(r));
         }
       }
       if (!ok) break;
-      n += chunks;
+      n += halves;
       more = next_piece();
     }
     } else if (warp < 4 * TILES + kValueWarps + kKeyWarps + 1) {
-    // ---------------- copies of codes and scales: one per lane ----------------
-    // lanes 0..3: 16 positions' key codes, 4..7: their scales, 8..11: the values' scales, 12..19: 8
-    // positions' value codes
-    const int what = lane < 4 ? 0 : lane < 8 ? 1 : lane < 12 ? 2 : 3;
-    const int part = lane < 12 ? lane & 3 : lane - 12, sixteen = lane < 12 ? part : (part >> 1) & 3;
-    const int bytes = what == 0 ? 16 * (D / 2) : what == 3 ? 8 * (D / 2) : 16 << log_sb;
-    const uint8_t* base = what == 0   ? a.c.codes[0]
-                          : what == 1 ? a.c.scales[0]
-                          : what == 2 ? a.c.scales[1]
-                                      : a.c.codes[1] + (part & 1) * (8 * (D / 2));
-    const int pitch = what == 0 || what == 3 ? 16 * (D / 2) : 16 << log_sb;  // of 16 positions
-    const uint32_t dst = s_raw + (what == 0   ? part * bytes
-                                  : what == 1 ? T::kRawKS + part * bytes
-                                  : what == 2 ? T::kRawVS + part * bytes
-                                              : T::kRawV + part * T::kOctet);
-    // the place of this lane's 16 positions of a chunk: the row of the cache (slots of one head) divided
-    // by 16, or -1
-    auto place = [&](int chunk) {
-      const int p = chunk * kChunk + 16 * sixteen;
+    // ---------------- copies of codes and scales ----------------
+    // Positions behind the end, or without a page, become zeros: a zero scale makes zeros of any codes,
+    // while what lies there may be NaN.
+    constexpr int CH = D / 32, PER = D / 64;  // 16-byte pieces of a position's codes; of 16, per lane
+    const int i0 = lane / CH, piece = lane % CH;
+    const uint32_t put_k = s_raw + i0 * (D / 2) + 16 * piece;
+    const uint32_t put_v = s_raw + T::kRawV + (i0 >> 3) * T::kOctet + (i0 & 7) * (D / 2) + 16 * piece;
+    const uint8_t* src_k = a.c.codes[0] + i0 * (D / 2) + 16 * piece;
+    const uint8_t* src_v = a.c.codes[1] + i0 * (D / 2) + 16 * piece;
+    const int sgr = lane >> log_sb, sfirst = (lane & ((1 << log_sb) - 1)) << (4 - log_sb);
+    // Lane i < 4 gets the place of the half's positions 16 i ..: the row of the cache (slots of one head)
+    // divided by 16, or -1.
+    auto place = [&](int half) {
+      const int p = half * kHalf + 16 * lane;
       int row = -1;
-      if (lane < 20 && p < k.end) {
+      if (lane < 4 && p < k.end) {
         const int64_t slot = a.table.slot(a.c, k.b, p);
         if (slot >= 0) row = (int)((slot + ((int64_t)k.h << a.c.page_shift)) >> 4);
       }
       return row;
     };
-    int issued = 0;
     while (more) {
       k = PieceOf(walk);
-      const int chunks = k.chunks;
+      const int halves = 2 * k.chunks, h0 = 2 * k.c0;
       bool ok = true;
-      int row = place(k.c0);
+      int next = place(h0);
 #pragma unroll 1
-      for (int j = 0; j < chunks; ++j) {
-        const int i = n + j, r = i % R;
-        const int here = row;
-        row = place(k.c0 + j + 1);
+      for (int j = 0; j < halves; ++j) {
+        const int i = n + j, r = i % R, p = (h0 + j) * kHalf;
+        const int rows = next;
+        next = place(h0 + j + 1);
         if (i >= R) ok = mbar_wait<20>(raw_empty(r), ((i / R) + 1) & 1, gave_up);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const uint32_t pages = __ballot_sync(0xffffffffu, here >= 0) & 15u;
-        if (lane == 0) {
-          s_pages[r] = pages;
-          mbar_arrive_expect_tx(raw_full(r), __popc(pages) * (2 * 16 * (D / 2) + 2 * (16 << log_sb)));
+        const uint32_t at = r * T::kRaw;
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          const int row = __shfl_sync(0xffffffffu, rows, gr);
+          const int left = row >= 0 ? k.end - (p + 16 * gr) : 0;  // positions that are there
+          const uint64_t from = (uint64_t)(uint32_t)max(row, 0) * (16 * (D / 2));
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            // positions i0 + e (32 / CH) of the 16
+            const int size = i0 + e * (32 / CH) < left ? 16 : 0;
+            const int pos = 16 * gr + e * (32 / CH);
+            cp_async16(put_k + at + pos * (D / 2), src_k + from + 512 * e, size);
+            cp_async16(put_v + at + (pos >> 3) * T::kOctet + (pos & 7) * (D / 2), src_v + from + 512 * e,
+                       size);
+          }
         }
-        __syncwarp();
-        if (here >= 0)
-          bulk_copy(dst + r * T::kRaw, base + (uint64_t)(uint32_t)here * pitch, bytes, raw_full(r));
-        issued = i + 1;
+        // scales: a piece of 16 bytes is those of 16 >> log_sb positions; 64 positions have at most 64
+        // pieces (32 and fewer but for head_dim 256 in blocks of 16)
+#pragma unroll
+        for (int e = 0; e < (D == 256 ? 2 : 1); ++e) {
+          const int gr = sgr + e * (32 >> log_sb);
+          const int row = __shfl_sync(0xffffffffu, rows, gr & 3);
+          if (gr < 4) {
+            const int left = row >= 0 ? k.end - (p + 16 * gr) - sfirst : 0;
+            const int size = min(max(left, 0), 16 >> log_sb) << log_sb;
+            const uint64_t from = ((uint64_t)(uint32_t)max(row, 0) << (4 + log_sb)) + (sfirst << log_sb);
+            const uint32_t to = s_raw + at + ((16 * gr + sfirst) << log_sb);
+            cp_async16(to + T::kRawKS, a.c.scales[0] + (size ? from : 0), size);
+            cp_async16(to + T::kRawVS, a.c.scales[1] + (size ? from : 0), size);
+          }
+        }
+        // this lane's arrival comes when its copies are there
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(raw_full(r))
+                     : "memory");
       }
       if (!ok) break;
-      n += chunks;
+      n += halves;
       more = next_piece();
     }
-    if (*gave_up) {  // copies in flight end before the block does
-      for (int i = max(0, issued - R); i < issued; ++i) {
-        int unused = 0;
-        mbar_wait(raw_full(i % R), (i / R) & 1, &unused);
-      }
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     } else {
     // ---------------- products (one elected thread) ----------------
-    if (more && elect_one()) {
-      auto scores = [&](int t, int i, int s) {  // of chunk i, its keys in stage s
-        const uint32_t qd = desc_low(s_q + t * T::kQ), kd = desc_low(s_k + s * T::kK);
-        const uint32_t d = tmem + T::kScoreCol + kChunk * (2 * t + (i & 1));
+    if (elect_one()) {
+      constexpr int P = S / 2;                   // stages of whole chunks
+      int tiles = TILES;                         // with rows, of the piece
+      int seen[2] = {0, 0}, pieces[2] = {0, 0};  // chunks and pieces so far, by tile
+      auto scores = [&](int t, int s) {
+        const uint32_t qd = desc_low(s_q + t * T::kQ), kd = desc_low(s_k + s * (2 * T::kK));
+        const uint32_t d = tmem + T::kScoreCol + kChunk * t;
         // 16 values of the head a step: 32 bytes on, after 64 the next 128-byte-wide block
         mma_ss<false>(d, qd, kd, T::kIdescS);
 #pragma unroll
-        for (int x = 1; x < D / 16; ++x)
-          mma_ss<true>(d, qd + (x >> 2) * ((128 * 128) >> 4) + 2 * (x & 3),
-                       kd + (x >> 2) * ((kChunk * 128) >> 4) + 2 * (x & 3), T::kIdescS);
-        tc_commit(s_full(t, i & 1));
-        if (t == TILES - 1) tc_commit(k_empty(s));
+        for (int x = 1; x < D / 16; ++x) {
+          const uint32_t on = (x >> 2) * ((128 * 128) >> 4) + 2 * (x & 3);
+          mma_ss<true>(d, qd + on, kd + on, T::kIdescS);
+        }
+        tc_commit(s_full(t));
+        if (t == tiles - 1) tc_commit(k_empty(s));
       };
-      auto outputs = [&](int t, int i, int s, bool add) {
-        const uint32_t vd = desc_low(s_v + s * T::kK);
-        const uint32_t pa = tmem + T::kScoreCol + kChunk * (2 * t + (i & 1));
+      auto outputs = [&](int t, int s, int half, bool add) {
+        const uint32_t vd = desc_low(s_v + (2 * s + half) * T::kK);
+        const uint32_t pa = tmem + T::kScoreCol + kChunk * t + 32 * half;
         mma_ts(tmem + T::kOutCol + D * t, pa, vd, T::kIdescO, add);
 #pragma unroll
-        for (int x = 1; x < kChunk / 16; ++x)
+        for (int x = 1; x < kHalf / 16; ++x)
           mma_ts(tmem + T::kOutCol + D * t, pa + 8 * x, vd + 2 * x, T::kIdescO, true);
-        tc_commit(o_done(t, i & 1));
-        if (t == TILES - 1) tc_commit(v_empty(s));
       };
       bool ok = true;
-      while (ok) {
-        const int chunks = walk.c1 - walk.c0;
-        for (int t = 0; t < TILES && ok; ++t) ok = mbar_wait(q_full(t), piece & 1, gave_up);
-        ok = ok && mbar_wait(k_full(n % S), (n / S) & 1, gave_up);
+      while (more && ok) {
+        const int chunks = walk.c1 - walk.c0, stop = n + chunks;
+        if constexpr (TILES > 1) {
+          const Seq seq(a, walk.b);
+          tiles = seq.count * group - walk.rt * T::kRows > 128 ? 2 : 1;
+        }
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+          if (ok && t < tiles) ok = mbar_wait(q_full(t), pieces[t]++ & 1, gave_up);
+        ok = ok && mbar_wait(k_full(n % P), (n / P) & 1, gave_up);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) scores(t, n, n % S);
-        const int stop = n + chunks;
+        for (int t = 0; t < TILES; ++t)
+          if (t < tiles) scores(t, n % P);
 #pragma unroll 1
-        for (; n < stop; ++n) {
-          const int s = n % S, s1 = (n + 1) % S;
-          const bool go = n + 1 < stop;
-          if (go && !(ok = mbar_wait(k_full(s1), ((n + 1) / S) & 1, gave_up))) break;
-          if (!(ok = mbar_wait(v_full(s), (n / S) & 1, gave_up))) break;
+        for (int c = n; c < stop; ++c) {
+          const int s = c % P, s1 = (c + 1) % P;
+          const bool go = c + 1 < stop;
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
-            tc_fence_after();
-            // into the buffer whose weights the outputs issued before this have read
-            if (go) scores(t, n + 1, s1);
-            if (!(ok = mbar_wait(p_full(t, n & 1), (n >> 1) & 1, gave_up))) break;
-            tc_fence_after();
-            outputs(t, n, s, n > stop - chunks);
+            if (t >= tiles || !ok) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (t == 0) ok = ok && mbar_wait(v_full(2 * s + half), (c / P) & 1, gave_up);
+              ok = ok && mbar_wait(p_full(t, half), seen[t] & 1, gave_up);
+              tc_fence_after();
+              if (ok) outputs(t, s, half, c > stop - chunks || half > 0);
+            }
+            if (t == tiles - 1) tc_commit(v_empty(s));
+            ++seen[t];
+            if (go) {
+              // (in order behind the outputs, which have read the weights there)
+              if (t == 0) ok = ok && mbar_wait(k_full(s1), ((c + 1) / P) & 1, gave_up);
+              tc_fence_after();
+              if (ok) scores(t, s1);
+            } else {
+              tc_commit(o_full(t));
+            }
           }
           if (!ok) break;
         }
-        ++piece;
-        if (!ok || !walk.next(a, cut)) break;
+        n = stop;
+        more = walk.next(a, cut);
       }
       tc_commit(done);  // also after giving up: every issued product
-    } else if (!more && lane == 0) {
-      tc_commit(done);
     }
     __syncwarp();
     }
