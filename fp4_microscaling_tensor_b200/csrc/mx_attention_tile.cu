@@ -23,8 +23,8 @@
 //     chunk at a time.
 // Keys, values and codes move in halves of a chunk.  Tensor memory per tile: 128 columns of scores
 // (weights overlay them), D columns of outputs.  (Two buffers of 64 columns would let a tile's scores run
-// ahead of its weights, but products 64 columns wide take as long as those 128 wide: measured 1198 us
-// for 2048 prompt tokens over 16384 positions, 64 heads on 8, against @@ us.)
+// ahead of its weights, but products 64 columns wide take as long as those 128 wide: measured 1164 us
+// for 2048 prompt tokens over 16384 positions, 64 heads on 8, against 1067 us.)
 //
 // Every wait is bounded (mbar_wait below): a block that gives up says so in a device counter
 // (mx_matmul_gave_up), lets its issued products finish, frees its tensor memory and returns; blocks do
@@ -409,11 +409,11 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           tc_wait_store();
         }
-        // ---- the chunk's maximum; its first 64 scores stay in registers
-        uint32_t v[64];
+        // ---- the chunk's maximum
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int h = 1; h >= 0; --h) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[64];
           tc_load32_async(t_s + 64 * h, v);
           tc_load32_async(t_s + 64 * h + 32, v + 32);
           tc_wait_load(v);
@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
         }
         __syncwarp();
-        // ---- weights: f16 pairs over the scores
+        // ---- weights: f16 pairs over the scores.  (Rolled up: unrolled, the warps' different code keeps
+        // missing the instruction caches.)
         auto weights = [&](int c, const uint32_t* x) {
           uint32_t w[16];
 #pragma unroll
@@ -463,22 +464,21 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
           }
           tc_store16(t_s + 16 * c, w);
         };
-        auto in_place = [&](int half) {
+        uint32_t v[32], u[32];
+        tc_load32_async(t_s, v);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          tc_wait_load(v);
+          tc_load32_async(t_s + 64 * half + 32, u);
+          weights(2 * half, v);
+          tc_wait_load(u);
+          if (half == 0) tc_load32_async(t_s + 64, v);
+          weights(2 * half + 1, u);
           tc_wait_store();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(tile, half));
-        };
-        weights(0, v);
-        tc_load32_async(t_s + 64, v);
-        weights(1, v + 32);
-        tc_wait_load(v);
-        tc_load32_async(t_s + 96, v + 32);
-        in_place(0);
-        weights(2, v);
-        tc_wait_load(v);
-        weights(3, v + 32);
-        in_place(1);
+        }
       }
       if (!ok) break;
       ok = mbar_wait(o_full(tile), piece & 1, gave_up);
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     const uint32_t src_s = s_raw + T::kRawVS + ((8 * oct) << log_sb) + (((D / 8) * run) >> log_block);
     while (more) {
       k = PieceOf(walk);
-      const int halves = 2 * k.chunks, h0 = 2 * k.c0;
+      const int halves = 2 * k.chunks;
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < halves; ++j) {
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     const uint32_t dst = s_k + (uint32_t)(pos >> 3) * 1024u + (uint32_t)(pos & 7) * 128u;
     while (more) {
       k = PieceOf(walk);
-      const int halves = 2 * k.chunks, h0 = 2 * k.c0;
+      const int halves = 2 * k.chunks;
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < halves; ++j) {
