@@ -45,7 +45,7 @@ constexpr int kStreamThreads = 32 * kWarps;
 constexpr float kSlack = 8.0f;
 
 
-constexpr int kUnit = 64, kStart = 4;  // of the stream kernel's Cut (start: 0 88, 2 86, 4 83 us for 64
+constexpr int kUnit = 64, kStart = 8;  // of the stream kernel's Cut (start: 0 88, 4 83, 8 79, 16 82 us for 64
                                       // sequences of 819 to 8191 positions)
 constexpr int kPart = 32;  // positions computed at a time (more outgrow the instruction cache)
 
