@@ -27,6 +27,12 @@ struct Cut {
   int rows, group, unit, start;
 };
 
+// a / b for a >= 0, b > 0 (the 64-bit division is an order of magnitude slower).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // A sequence's numbers, cut to what is there: len positions, of which the newest `count` are this
 // call's tokens, from position base on (negative where the sequence is shorter than its count).
 struct Seq {
@@ -43,7 +49,7 @@ struct Seq {
   }
   __device__ __forceinline__ int end(const AttnArgs& a, const Cut& c, int rt) const {
     if (a.tree) return len;
-    const int64_t last = ((int64_t)(rt + 1) * c.rows - 1) / c.group;  // the tile's last token
+    const int64_t last = divide((int64_t)(rt + 1) * c.rows - 1, c.group);  // the tile's last token
     return max(0, (int)min((int64_t)len, base + min((int64_t)count - 1, last) + 1));
   }
 };
@@ -52,41 +58,44 @@ __device__ __forceinline__ int units_of(const Cut& c, int end) {
   return c.start + max(1, (end + c.unit - 1) / c.unit);
 }
 
-// Units of one key/value head of sequence b.
-__device__ __forceinline__ int64_t head_units(const AttnArgs& a, int64_t b, const Cut& c) {
-  const Seq s(a, b);
+// Units of one key/value head of a sequence: the part that lane `sub` of `lanes` adds up.
+__device__ __forceinline__ int64_t head_units(const AttnArgs& a, const Seq& s, const Cut& c, int sub,
+                                              int lanes) {
   const int tiles = s.tiles(c);
-  if (a.tree || tiles <= 1) return tiles ? (int64_t)tiles * units_of(c, s.end(a, c, 0)) : 0;
+  if (a.tree || tiles <= 1)
+    return tiles && sub == 0 ? (int64_t)tiles * units_of(c, s.end(a, c, 0)) : 0;
   int64_t n = 0;
-  for (int rt = 0; rt < tiles; ++rt) n += units_of(c, s.end(a, c, rt));
+  for (int rt = sub; rt < tiles; rt += lanes) n += units_of(c, s.end(a, c, rt));
   return n;
-}
-
-// a / b for a >= 0, b > 0 (the 64-bit division is an order of magnitude slower).
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
 }
 
 // Where a thread block's share of the list begins, and how long the list is.
 struct Share {
-  int64_t b;          // sequence of the share's first unit
-  int64_t off;        // the unit's place among the sequence's
-  int64_t lo, hi, total;
+  int64_t b;          // the segment of the share's first unit,
+  int h, rt;
+  int at;             // and the unit's place in it
   int blocks;         // how many blocks have a share that is not empty: the first ones
+  int64_t lo, hi, total;
 };
 
-// All THREADS threads; scratch: THREADS / 32 values.  Each thread sums a run of sequences; the one
-// whose run holds the share's first unit walks it again.
+// All THREADS threads; scratch: THREADS / 32 values.  A group of threads (32, fewer for many sequences,
+// then one for a run of them) adds up the tiles of a sequence; the warp in whose run the share's first
+// unit is looks the tile up, 32 at a time.  (One thread for a sequence took 10 us for 64 tiles.)
 template <int THREADS>
 __device__ __forceinline__ void find_share(const AttnArgs& a, const Cut& c, int cta, int ctas,
                                            int64_t* scratch, Share* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per = (a.batch + THREADS - 1) / THREADS;
-  const int64_t b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+  int lanes = 32;
+  while (lanes > 1 && a.batch * lanes > THREADS) lanes >>= 1;
+  const int sub = tid & (lanes - 1), gid = tid / lanes;
+  const int64_t per = divide(a.batch + THREADS / lanes - 1, THREADS / lanes);  // 1 if lanes > 1
+  const int64_t b0 = min(a.batch, gid * per), b1 = min(a.batch, b0 + per);
   int64_t sum = 0;
-  for (int64_t b = b0; b < b1; ++b) sum += head_units(a, b, c) * a.c.kv_heads;
-  int64_t incl = sum;
+  for (int64_t b = b0; b < b1; ++b) sum += head_units(a, Seq(a, b), c, sub, lanes);
+  for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  int64_t units = sum;  // of a key/value head, in all the sequences of the run
+  sum *= a.c.kv_heads;
+  int64_t incl = sub == 0 ? sum : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -105,16 +114,42 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, const Cut& c, int 
   const int64_t lo = cta < n ? divide(total * cta, n) : total;
   const int64_t hi = cta < n ? divide(total * (cta + 1), n) : total;
   const int64_t first = before + incl - sum;
-  if (lo < hi && lo >= first && lo < first + sum) {
+  const uint32_t who = __ballot_sync(0xffffffffu, lo < hi && lo >= first && lo < first + sum);
+  if (who) {
     int64_t at = lo - first, b = b0;
-    for (; b < b1; ++b) {
-      const int64_t m = head_units(a, b, c) * a.c.kv_heads;
-      if (at < m) break;
-      at -= m;
+    if (lanes == 1 && (who >> lane & 1)) {
+      for (;; ++b) {
+        units = head_units(a, Seq(a, b), c, 0, 1);
+        if (at < units * a.c.kv_heads) break;
+        at -= units * a.c.kv_heads;
+      }
     }
-    *out = {b, at, lo, hi, total, n};
+    const int src = __ffs(who) - 1;
+    at = __shfl_sync(0xffffffffu, at, src);
+    b = __shfl_sync(0xffffffffu, b, src);
+    units = __shfl_sync(0xffffffffu, units, src);
+    const int h = (int)divide(at, units);
+    at -= h * units;
+    const Seq s(a, b);
+    const int tiles = s.tiles(c);
+    for (int rt0 = 0; rt0 < tiles; rt0 += 32) {
+      const int mine = rt0 + lane < tiles ? units_of(c, s.end(a, c, rt0 + lane)) : 0;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, upto > at);
+      if (past) {
+        if (lane == __ffs(past) - 1)
+          *out = {b, h, rt0 + lane, (int)at - (upto - mine), n, lo, hi, total};
+        break;
+      }
+      at -= __shfl_sync(0xffffffffu, upto, 31);
+    }
   }
-  if (tid == 0 && lo >= hi) *out = {0, 0, 0, 0, total, n};  // an empty share
+  if (tid == 0 && lo >= hi) *out = {0, 0, 0, 0, n, 0, 0, total};  // an empty share
   __syncthreads();
 }
 
@@ -144,19 +179,15 @@ struct Walk {
   __device__ __forceinline__ bool begin(const AttnArgs& a, const Cut& c, const Share& sh) {
     if (sh.lo >= sh.hi) return false;
     b = sh.b;
+    h = sh.h;
+    rt = sh.rt;
     const Seq s(a, b);
-    const int64_t per = head_units(a, b, c);
-    h = (int)divide(sh.off, per);
-    int64_t at = sh.off - h * per;
-    rt = 0;
-    for (int m = units_of(c, s.end(a, c, 0)); at >= m;
-         m = units_of(c, s.end(a, c, ++rt)))
-      at -= m;
+    int at = sh.at;
     u0 = sh.lo - at;
     if (at <= c.start) at = 0;
     left = sh.hi - (u0 + at);
     if (left <= c.start && at == 0) return false;
-    set(a, c, s, (int)at);
+    set(a, c, s, at);
     return true;
   }
   // The next piece; false if there is none.
@@ -187,11 +218,11 @@ cudaError_t run_tile(const AttnArgs& a, cudaStream_t stream, int* launches);
 
 // ---- workspace: one record per thread block, then two partial results per thread block ------------
 
-// Written by the block that holds a split segment's first units: the segment, and the blocks that
-// hold its pieces; last < 0: nothing to join.
+// Written by the block that holds a split segment's first units: the segment, the last of the blocks
+// that hold its pieces, and its query rows; last < 0: nothing to join.
 struct Record {
   int64_t b;
-  int h, rt, last, pad;
+  int h, rt, last, rows;
 };
 static_assert(sizeof(Record) == 24, "record layout");
 
@@ -300,34 +331,81 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, const Seq& s, int t, uin
 
 namespace {
 
-// Joins the pieces of the segment that block blockIdx.x began and did not end: blocks c .. last hold
-// one each.  blockIdx.y: a quarter of the head dimension.  A thread holds four outputs of a row and
-// every K-th piece; the K runs are added up in order.
-template <int D, int R>
-__global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ AttnArgs a, int ctas,
-                                                        float gv) {
-  constexpr int kItems = R * (D / 16);               // float4 outputs of a quarter
-  constexpr int kPer = kItems < 256 ? kItems : 256;  // threads per run
-  constexpr int K = 256 / kPer;
-  __shared__ float4 s_o[K][kPer];
-  __shared__ float s_m[K][kPer], s_l[K][kPer];
+constexpr int kJoinThreads = 256, kMostRuns = 16;
+
+// How many threads share the pieces of an output, four pieces each (a power of two).
+__device__ __forceinline__ int log_runs(int pieces) {
+  int k = 0;
+  while ((4 << k) < pieces && (1 << k) < kMostRuns) ++k;
+  return k;
+}
+
+// Joins the pieces of the segments that are split: that of record c is in blocks c .. last, one piece
+// each.  The work is a list of steps of kJoinThreads threads, over all records; every block adds their
+// numbers up and takes every gridDim.x-th.  A thread holds four outputs of a row and a run of pieces;
+// the runs are added up in order.  (With a block for each record and quarter of the head dimension, 2
+// segments of 60 pieces took 70 us.)
+template <int D, int R, int MAX_CTAS>
+__global__ void __launch_bounds__(kJoinThreads) k_attention_join(const __grid_constant__ AttnArgs a,
+                                                                 int ctas, float gv) {
+  constexpr int kPer = (MAX_CTAS + kJoinThreads - 1) / kJoinThreads;  // records per thread
+  __shared__ int s_warp[kJoinThreads / 32];
+  __shared__ Record s_rec;
+  __shared__ int s_first, s_step;  // the block that began the segment; the step's place among its steps
+  __shared__ float4 s_o[kJoinThreads];
+  __shared__ float s_m[kJoinThreads], s_l[kJoinThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (The next kernel is not launched early: blocks of the stream kernel that come while this one's leave
+  // spread unevenly over the SMs, and 59 us became of 43 for calls in a row, 16 sequences of up to 4000
+  // positions, head_dim 64.)
   griddep_wait();
-  griddep_launch_next();
-  const int c = blockIdx.x;
-  const Record rec = reinterpret_cast<const Record*>(a.workspace)[c];
-  if (rec.last < 0) return;
+  Record recs[kPer];
+  int steps[kPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int c = tid + k * kJoinThreads;
+    steps[k] = 0;
+    if (c < ctas) {
+      recs[k] = reinterpret_cast<const Record*>(a.workspace)[c];
+      if (recs[k].last >= 0)
+        steps[k] = ((recs[k].rows * (D / 4) << log_runs(recs[k].last - c + 1)) + kJoinThreads - 1) /
+                   kJoinThreads;
+    }
+    sum += steps[k];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < warp) incl += s_warp[w];
+    total += s_warp[w];
+  }
+
   const int group = a.heads / a.c.kv_heads;
-  const int count = a.count ? (int)min((int64_t)max(a.count[rec.b], 0), a.tokens) : (int)a.tokens;
-  const int rows = min((int64_t)R, (int64_t)count * group - (int64_t)rec.rt * R);
-  const int n = rec.last - c + 1;
-  for (int i0 = 0; i0 < kItems; i0 += kPer) {
-    const int i = i0 + (int)threadIdx.x % kPer, run = threadIdx.x / kPer;
-    const int r = i / (D / 16), d = blockIdx.y * (D / 4) + 4 * (i % (D / 16));
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int at = u - (incl - sum);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (at >= 0 && at < steps[k]) s_rec = recs[k], s_first = tid + k * kJoinThreads, s_step = at;
+      at -= steps[k];
+    }
+    __syncthreads();
+    const Record rec = s_rec;
+    const int c = s_first, n = rec.last - c + 1, lk = log_runs(n), items = kJoinThreads >> lk;
+    const int i = s_step * items + (tid & (items - 1)), run = tid / items;
+    const int r = i / (D / 4), d = 4 * (i % (D / 4));
     float mx = -INFINITY, l = 0.0f;
     float4 y = make_float4(0, 0, 0, 0);
-    if (r < rows) {
+    if (r < rec.rows) {
       // pieces run * per .. : an order that depends on their number only
-      const int per = (n + K - 1) / K, x1 = min(n, (run + 1) * per);
+      const int per = (n + (1 << lk) - 1) >> lk, x1 = min(n, (run + 1) * per);
       for (int x0 = run * per; x0 < x1; x0 += 4) {
         float pm[4], pl[4];
         float4 po[4];
@@ -352,29 +430,26 @@ __global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ 
         }
       }
     }
-    if constexpr (K > 1) {
-      const int j = threadIdx.x % kPer;
-      s_m[run][j] = mx, s_l[run][j] = l, s_o[run][j] = y;
+    if (lk > 0) {
+      s_m[tid] = mx, s_l[tid] = l, s_o[tid] = y;
       __syncthreads();
       if (run == 0) {
         float mn = mx;
-#pragma unroll
-        for (int x = 1; x < K; ++x) mn = fmaxf(mn, s_m[x][j]);
+        for (int x = 1; x < 1 << lk; ++x) mn = fmaxf(mn, s_m[x * items + tid]);
         const float mu = mn == -INFINITY ? 0.0f : mn;
         l = 0.0f, y = make_float4(0, 0, 0, 0);
-#pragma unroll
-        for (int x = 0; x < K; ++x) {
-          const float w = ex2(s_m[x][j] - mu);
-          const float4 v = s_o[x][j];
-          l += s_l[x][j] * w;
+        for (int x = 0; x < 1 << lk; ++x) {
+          const float w = ex2(s_m[x * items + tid] - mu);
+          const float4 v = s_o[x * items + tid];
+          l += s_l[x * items + tid] * w;
           y.x += v.x * w, y.y += v.y * w, y.z += v.z * w, y.w += v.w * w;
         }
         mx = mn;
       }
     }
-    if (r < rows && run == 0) {
+    if (r < rec.rows && run == 0) {
       const int64_t row = (int64_t)rec.rt * R + r;
-      const int t = (int)(row / group), head = rec.h * group + (int)(row % group);
+      const int t = (int)divide(row, group), head = rec.h * group + (int)(row - (int64_t)t * group);
       const float f = l == 0.0f ? 0.0f : gv / l;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + row_offset(a.out, rec.b, t, head) +
                                 d) =
@@ -384,18 +459,18 @@ __global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ 
             l == 0.0f ? -INFINITY
                       : ((mx == -INFINITY ? 0.0f : mx) + log2f(l)) * 0.6931471805599453f;
     }
-    if constexpr (K > 1) __syncthreads();
+    __syncthreads();
   }
 }
 
-// Launches the join behind a kernel of `ctas` blocks (its blocks only read a record where nothing was
-// split).
-template <int D, int R>
-cudaError_t launch_join(const AttnArgs& a, int ctas, int scale_shift, cudaStream_t stream,
+// Launches the join behind a kernel of `ctas` blocks (whose blocks only read the records where nothing
+// was split).
+template <int D, int R, int MAX_CTAS>
+cudaError_t launch_join(const AttnArgs& a, int ctas, int sms, int scale_shift, cudaStream_t stream,
                         int* launches) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, 4);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)(4 * (ctas < sms ? ctas : sms)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -405,7 +480,7 @@ cudaError_t launch_join(const AttnArgs& a, int ctas, int scale_shift, cudaStream
   const uint32_t g = a.c.g_bits[1];
   const float gv = ldexpf(g >> 10 ? (float)(1024 + (g & 1023)) : (float)g,
                           (g >> 10 ? (int)(g >> 10) - 25 : -24) + scale_shift);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attention_join<D, R>, a, ctas, gv);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attention_join<D, R, MAX_CTAS>, a, ctas, gv);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

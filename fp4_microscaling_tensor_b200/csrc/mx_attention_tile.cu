@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       if (lane == 0) mbar_arrive(q_full(tile));
 
       const uint64_t word = in && a.tree ? a.tree[k.b * a.tokens + t] : 0;
-      const int plain_end = min(k.end, seq.base + 1);
+      // what every row of the warp sees: up to its first row's token (a tree's rows: the old positions)
+      const int first = a.tree ? 0 : (row - lane) / group;
+      const int plain_end = min(k.end, seq.base + first + 1);
       const int chunks = k.chunks;
       float m = -INFINITY, mu = 0.0f, lim = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);
@@ -524,7 +526,8 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       }
       if (threadIdx.x == 0 && k.c0 == 0 && !whole)
         reinterpret_cast<Record*>(a.workspace)[cta] = {
-            k.b, k.h, k.rt, block_of(walk.u0 + walk.n + kTileStart - 1, s_share), 0};
+            k.b, k.h, k.rt, block_of(walk.u0 + walk.n + kTileStart - 1, s_share),
+            min(T::kRows, rows - k.rt * T::kRows)};
       tc_fence_before();
       n += chunks;
       ++piece;
@@ -840,7 +843,7 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream, int* launches) {
   e = launch_pdl_smem(kern, ctas, T::kThreads, T::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  return launch_join<D, T::kRows>(a, ctas, kScaleShift<FMT>, stream, launches);
+  return launch_join<D, T::kRows, kMaxTileCtas>(a, ctas, sms, kScaleShift<FMT>, stream, launches);
 }
 
 template <int D, int TILES>

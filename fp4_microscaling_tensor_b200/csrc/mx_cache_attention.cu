@@ -528,7 +528,7 @@ struct Stream {
     seq = Seq(a, b);
     end = p1;
     holes = false;
-    plain_end = min(end, seq.base + 1);
+    plain_end = min(end, seq.base + (a.tree ? 0 : row0 / group) + 1);
     ahead = p0;
     rows = page_rows(p0);
     rows_next = page_rows(p0 + 512);
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
       const bool whole = k.whole();
       float* part = partial(a, ctas, R, D, 2 * cta + (k.c0 == 0));
       if (k.c0 == 0 && !whole)
-        mine = {b, h, k.rt, block_of(k.u0 + k.n + kStart - 1, sh), 0};
+        mine = {b, h, k.rt, block_of(k.u0 + k.n + kStart - 1, sh), rows};
       const bool more = k.next(a, cut);
       if (more) begin();
       __syncthreads();
@@ -689,7 +689,7 @@ int row_groups(int64_t rows, int dim) {
   return nt < most ? nt : most;
 }
 
-constexpr int kMaxStreamCtas = 4 * 160;  // thread blocks at most: 4 per SM
+constexpr int kMaxStreamCtas = 3 * 160;  // thread blocks at most: 3 per SM
 
 template <int D, int NT, int FMT, bool N16>
 cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches) {
@@ -713,7 +713,7 @@ cudaError_t launch_stream(const AttnArgs& a, cudaStream_t stream, int* launches)
   e = launch_pdl_smem(kern, ctas, kStreamThreads, smem, stream, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  return launch_join<D, 8 * NT>(a, ctas, kScaleShift<FMT>, stream, launches);
+  return launch_join<D, 8 * NT, kMaxStreamCtas>(a, ctas, sms, kScaleShift<FMT>, stream, launches);
 }
 
 template <int D, int NT>
