@@ -37,6 +37,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 // call's tokens, from position base on (negative where the sequence is shorter than its count).
 struct Seq {
   int len, count, base;
+  Seq() = default;
   __device__ __forceinline__ Seq(const AttnArgs& a, int64_t b) {
     const int64_t reach = a.table.width << a.c.page_shift;  // at most 2^30
     len = (int)min((int64_t)max(a.length[b], 0), reach);
@@ -166,8 +167,9 @@ struct Walk {
   int end;             // positions the tile's rows see at most
   int64_t left;        // units of the share behind this piece
   int64_t u0;          // the list's place of the segment's first unit
-  __device__ __forceinline__ void set(const AttnArgs& a, const Cut& c, const Seq& s, int at) {
-    end = s.end(a, c, rt);
+  Seq seq;
+  __device__ __forceinline__ void set(const AttnArgs& a, const Cut& c, int at) {
+    end = seq.end(a, c, rt);
     const int units = units_of(c, end);
     const int take = (int)min((int64_t)(units - at), left);
     n = units - c.start;
@@ -181,28 +183,28 @@ struct Walk {
     b = sh.b;
     h = sh.h;
     rt = sh.rt;
-    const Seq s(a, b);
+    seq = Seq(a, b);
     int at = sh.at;
     u0 = sh.lo - at;
     if (at <= c.start) at = 0;
     left = sh.hi - (u0 + at);
     if (left <= c.start && at == 0) return false;
-    set(a, c, s, at);
+    set(a, c, at);
     return true;
   }
   // The next piece; false if there is none.
   __device__ __forceinline__ bool next(const AttnArgs& a, const Cut& c) {
     if (left <= c.start) return false;
     u0 += n + c.start;
-    if (++rt >= Seq(a, b).tiles(c)) {
+    if (++rt >= seq.tiles(c)) {
       rt = 0;
       if (++h >= a.c.kv_heads) {
         h = 0;
-        do ++b;
-        while (Seq(a, b).tiles(c) == 0);
+        do seq = Seq(a, ++b);
+        while (seq.tiles(c) == 0);
       }
     }
-    set(a, c, Seq(a, b), 0);
+    set(a, c, 0);
     return true;
   }
   __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == n; }

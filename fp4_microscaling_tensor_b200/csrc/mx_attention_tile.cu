@@ -293,10 +293,18 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
     const uint32_t t_s = tmem + T::kScoreCol + kChunk * tile + t_lane;
     const uint32_t t_o = tmem + T::kOutCol + D * tile + t_lane;
     const float gv = fp16_bits_to_float(a.c.g_bits[1]) * (float)(1 << kScaleShift<FMT>);
+    // The warp's 32 rows in the queries' place, 2 D bytes each: 16-byte piece i of row rr.  kLanes lanes
+    // move a row to or from global memory, kTogether rows at a time.
+    constexpr int kLanes = D / 8, kTogether = 32 / kLanes;
+    const int piece_of = lane % kLanes;
+    const uint32_t q_rows = s_q + tile * T::kQ + (uint32_t)(warp & 3) * 4096u;
+    auto own_rows = [&](int rr, int i) {
+      return q_rows + (uint32_t)(i >> 3) * 16384u + (uint32_t)rr * 128u + (uint32_t)((i ^ rr) & 7) * 16u;
+    };
     if (threadIdx.x == 0) reinterpret_cast<Record*>(a.workspace)[cta].last = -1;
     while (more) {
       const PieceOf k(walk);
-      const Seq seq(a, k.b);
+      const Seq seq = walk.seq;
       const int rows = seq.count * group, row = k.rt * T::kRows + 128 * tile + r;
       if (TILES > 1 && rows - k.rt * T::kRows <= 128 * tile) {  // no rows here (tile 0 always has some)
         more = next_piece();
@@ -306,37 +314,46 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       const int t = in ? row / group : 0, head = k.h * group + (in ? row % group : 0);
       float mult;
       {
-        // the row times a power of two that brings its largest magnitude to [2^14, 2^15), as f16
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) +
-                                                          row_offset(a.q, k.b, t, head));
-        uint32_t mx = 0;
-        const bool live = in && a.scale != 0.0f;
-        if (live) {
-#pragma unroll 8
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = __ldg(src + i);
-            mx = max(mx, max(max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu),
-                                 max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)),
-                             max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu),
-                                 max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu))));
+        // the row times a power of two that brings its largest magnitude to [2^14, 2^15), as f16.
+        // D / 8 lanes read a row together (a lane reading a row of its own took four times as long);
+        // in the end every lane keeps the power of its row.
+        const int64_t off = row_offset(a.q, k.b, t, head);
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        int f = 0;
+#pragma unroll 1
+        for (int x0 = 0; x0 < kLanes; x0 += 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int rr = (x0 + x) * kTogether + lane / kLanes;
+            const int64_t at = __shfl_sync(0xffffffffu, off, rr);
+            v[x] = make_uint4(0, 0, 0, 0);
+            if (row - lane + rr < rows && a.scale != 0.0f)
+              v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + at) +
+                           piece_of);
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int rr = (x0 + x) * kTogether + lane / kLanes;
+            uint32_t mx = max(max(max(v[x].x & 0x7FFFu, (v[x].x >> 16) & 0x7FFFu),
+                                  max(v[x].y & 0x7FFFu, (v[x].y >> 16) & 0x7FFFu)),
+                              max(max(v[x].z & 0x7FFFu, (v[x].z >> 16) & 0x7FFFu),
+                                  max(v[x].w & 0x7FFFu, (v[x].w >> 16) & 0x7FFFu)));
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int fr = mx == 0 || mx >= 0x7F80u ? 0 : 141 - max((int)(mx >> 7), 1);
+            const int mine = __shfl_sync(0xffffffffu, fr, (lane % kTogether) * kLanes);
+            if (lane / kTogether == x0 + x) f = mine;
+            const float s1 = __uint_as_float((uint32_t)(127 + fr / 2) << 23);
+            const float s2 = __uint_as_float((uint32_t)(127 + fr - fr / 2) << 23);
+            auto half2 = [&](uint32_t w) {
+              return pack_f16x2(bf16lo(w) * s1 * s2, bf16hi(w) * s1 * s2) ^ flip;
+            };
+            st_shared16(own_rows(rr, piece_of), half2(v[x].x), half2(v[x].y), half2(v[x].z),
+                        half2(v[x].w));
           }
         }
-        const int f = mx == 0 || mx >= 0x7F80u ? 0 : 141 - max((int)(mx >> 7), 1);
         const int f1 = f / 2, f2 = f - f1;
-        const float s1 = __uint_as_float((uint32_t)(127 + f1) << 23);
-        const float s2 = __uint_as_float((uint32_t)(127 + f2) << 23);
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-        const uint32_t dst = s_q + tile * T::kQ + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = __ldg(src + i);
-          auto half2 = [&](uint32_t w) {
-            return pack_f16x2(bf16lo(w) * s1 * s2, bf16hi(w) * s1 * s2) ^ (live ? flip : 0u);
-          };
-          st_shared16(dst + (i >> 3) * 16384u + ((((uint32_t)i & 7u) ^ (r & 7u)) << 4), half2(v.x),
-                      half2(v.y), half2(v.z), half2(v.w));
-        }
         const float gk = fp16_bits_to_float(a.c.g_bits[0]) * (float)(1 << kScaleShift<FMT>);
         mult = (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * gk * 1.4426950408889634f) *
                __uint_as_float((uint32_t)(127 - f1) << 23) * __uint_as_float((uint32_t)(127 - f2) << 23);
@@ -490,29 +507,44 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       const bool whole = walk.whole();
       float* part = partial(a, ctas, T::kRows, D, 2 * cta + (k.c0 == 0));
       const float f = whole ? (sum == 0.0f ? 0.0f : gv / sum) : 1.0f;
-      uint16_t* out = static_cast<uint16_t*>(a.out.p) + row_offset(a.out, k.b, t, head);
       const int pr = 128 * tile + r;
+      // The outputs (bf16), or D / 2 of a piece's (float32) at a time, go through the place of the
+      // queries, which the products have read, so that rows leave as a whole.
+      const int64_t off = row_offset(a.out, k.b, t, head);
 #pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t x[16];
-        __syncwarp();
-        tc_load16(t_o + 16 * c, x);
-        if (!in) continue;
-        float y[16];
+      for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; c += whole ? 1 : 2) {
+          uint32_t x[16];
+          tc_load16(t_o + 16 * (whole ? c : (D / 32) * pass + (c >> 1)), x);
+          if (whole) {
+            uint32_t y[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(x[i]) * f;
-        if (whole) {
+            for (int i = 0; i < 8; ++i)
+              y[i] = pack_bf16x2(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
+            st_shared16(own_rows(lane, 2 * c), y[0], y[1], y[2], y[3]);
+            st_shared16(own_rows(lane, 2 * c + 1), y[4], y[5], y[6], y[7]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 16; i += 8)
-            *reinterpret_cast<uint4*>(out + 16 * c + i) =
-                make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
-                           pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(part + 2 * T::kRows + (size_t)pr * D + 16 * c + i) =
-                make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            for (int i = 0; i < 4; ++i)
+              st_shared16(own_rows(lane, 2 * c + i), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int x = 0; x < kLanes; ++x) {
+          const int rr = x * kTogether + lane / kLanes;
+          const int64_t at = __shfl_sync(0xffffffffu, off, rr);
+          uint32_t v[4];
+          lds<16>(own_rows(rr, piece_of), v);
+          if (row - lane + rr < rows) {
+            char* dst = whole ? static_cast<char*>(a.out.p) + 2 * at
+                              : reinterpret_cast<char*>(part + 2 * T::kRows +
+                                                        (size_t)(pr - lane + rr) * D + (D / 2) * pass);
+            reinterpret_cast<uint4*>(dst)[piece_of] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        __syncwarp();
       }
       if (in) {
         if (whole) {
@@ -766,8 +798,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       while (more && ok) {
         const int chunks = walk.c1 - walk.c0, stop = n + chunks;
         if constexpr (TILES > 1) {
-          const Seq seq(a, walk.b);
-          tiles = seq.count * group - walk.rt * T::kRows > 128 ? 2 : 1;
+          tiles = walk.seq.count * group - walk.rt * T::kRows > 128 ? 2 : 1;
         }
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
