@@ -314,46 +314,43 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       const int t = in ? row / group : 0, head = k.h * group + (in ? row % group : 0);
       float mult;
       {
-        // the row times a power of two that brings its largest magnitude to [2^14, 2^15), as f16.
-        // D / 8 lanes read a row together (a lane reading a row of its own took four times as long);
-        // in the end every lane keeps the power of its row.
+        // the row times a power of two that brings its largest magnitude to [2^14, 2^15), as f16.  D / 8
+        // lanes copy a row together into its place, where the lane whose row it is scales it.  (Rolled
+        // up, like all that runs once a piece: what has to come into the instruction caches costs more
+        // than it does.)
         const int64_t off = row_offset(a.q, k.b, t, head);
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-        int f = 0;
-#pragma unroll 1
-        for (int x0 = 0; x0 < kLanes; x0 += 8) {
-          uint4 v[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int rr = (x0 + x) * kTogether + lane / kLanes;
-            const int64_t at = __shfl_sync(0xffffffffu, off, rr);
-            v[x] = make_uint4(0, 0, 0, 0);
-            if (row - lane + rr < rows && a.scale != 0.0f)
-              v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + at) +
-                           piece_of);
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int rr = (x0 + x) * kTogether + lane / kLanes;
-            uint32_t mx = max(max(max(v[x].x & 0x7FFFu, (v[x].x >> 16) & 0x7FFFu),
-                                  max(v[x].y & 0x7FFFu, (v[x].y >> 16) & 0x7FFFu)),
-                              max(max(v[x].z & 0x7FFFu, (v[x].z >> 16) & 0x7FFFu),
-                                  max(v[x].w & 0x7FFFu, (v[x].w >> 16) & 0x7FFFu)));
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int fr = mx == 0 || mx >= 0x7F80u ? 0 : 141 - max((int)(mx >> 7), 1);
-            const int mine = __shfl_sync(0xffffffffu, fr, (lane % kTogether) * kLanes);
-            if (lane / kTogether == x0 + x) f = mine;
-            const float s1 = __uint_as_float((uint32_t)(127 + fr / 2) << 23);
-            const float s2 = __uint_as_float((uint32_t)(127 + fr - fr / 2) << 23);
-            auto half2 = [&](uint32_t w) {
-              return pack_f16x2(bf16lo(w) * s1 * s2, bf16hi(w) * s1 * s2) ^ flip;
-            };
-            st_shared16(own_rows(rr, piece_of), half2(v[x].x), half2(v[x].y), half2(v[x].z),
-                        half2(v[x].w));
-          }
+#pragma unroll 2
+        for (int x = 0; x < kLanes; ++x) {
+          const int rr = x * kTogether + lane / kLanes;
+          const int64_t at = __shfl_sync(0xffffffffu, off, rr);
+          const bool there = row - lane + rr < rows && a.scale != 0.0f;
+          cp_async16(own_rows(rr, piece_of), static_cast<const uint16_t*>(a.q.p) + (there ? at + 8 * piece_of : 0),
+                     there ? 16 : 0);
         }
-        const int f1 = f / 2, f2 = f - f1;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        uint32_t mx = 0;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t v[4];
+          lds<16>(own_rows(lane, i), v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+        }
+        const int f = mx == 0 || mx >= 0x7F80u ? 0 : 141 - max((int)(mx >> 7), 1);
+        const int f1 = f / 2, f2 = f - f1;  // |f| may be 140: two steps
+        const float s1 = __uint_as_float((uint32_t)(127 + f1) << 23);
+        const float s2 = __uint_as_float((uint32_t)(127 + f2) << 23);
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll 2
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t v[4];
+          lds<16>(own_rows(lane, i), v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_f16x2(bf16lo(v[e]) * s1 * s2, bf16hi(v[e]) * s1 * s2) ^ flip;
+          st_shared16(own_rows(lane, i), v[0], v[1], v[2], v[3]);
+        }
         const float gk = fp16_bits_to_float(a.c.g_bits[0]) * (float)(1 << kScaleShift<FMT>);
         mult = (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * gk * 1.4426950408889634f) *
                __uint_as_float((uint32_t)(127 - f1) << 23) * __uint_as_float((uint32_t)(127 - f2) << 23);
