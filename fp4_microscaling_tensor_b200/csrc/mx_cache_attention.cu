@@ -681,10 +681,12 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
   if (threadIdx.x == 0) *rec = mine;
 }
 
-// Query rows per tile: 8, 16 or 32, as many as there are (a tile's rows share one pass over the
-// cache); 16 at most for head_dim 256, whose accumulators fill the registers.
+// Query rows per tile: 8, 16 or 32, as many as there are (a tile's rows share one pass over the cache);
+// 16 at most for head_dim 128 and 256, where the accumulators of 32 spill (16 sequences of up to 8000
+// positions, 32 rows per key/value head, head_dim 128: two passes of 16 rows 85 us, one of 32 146 us;
+// head_dim 64: one pass 56 us).
 int row_groups(int64_t rows, int dim) {
-  const int most = dim == 256 ? 2 : 4;
+  const int most = dim == 64 ? 4 : 2;
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   return nt < most ? nt : most;
 }
@@ -729,7 +731,7 @@ template <int D>
 cudaError_t dispatch_rows(const AttnArgs& a, cudaStream_t stream, int* launches) {
   const int nt = row_groups(a.tokens * (a.heads / a.c.kv_heads), D);
   if (nt == 1) return dispatch_format<D, 1>(a, stream, launches);
-  if constexpr (D < 256) {
+  if constexpr (D == 64) {
     if (nt == 4) return dispatch_format<D, 4>(a, stream, launches);
   }
   return dispatch_format<D, 2>(a, stream, launches);
@@ -738,7 +740,10 @@ cudaError_t dispatch_rows(const AttnArgs& a, cudaStream_t stream, int* launches)
 }  // namespace
 }  // namespace attn
 
-// Above this many query rows per key/value head the products outweigh the reading of the cache.
+// Above this many query rows per key/value head the tile kernel takes over, whose time hardly depends on
+// the rows up to 128.  32 rows there and here (16 sequences of up to 8000 positions): head_dim 64 100 and
+// 56 us, 128 117 and 85, 256 302 and 201; of up to 600: 27 and 24, 34 and 26, 53 and 44.  64 rows: 120
+// there, 250 here (head_dim 128).
 static constexpr int kStreamRows = 32;
 
 size_t attention_workspace_bytes(int64_t batch, int64_t tokens, int heads, int kv_heads,
