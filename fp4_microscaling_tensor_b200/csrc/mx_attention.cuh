@@ -1,14 +1,15 @@
 // mx_attention.cuh -- what the attention kernels over the FP4 cache share: how the work is cut, the
 // partial results of pieces, and small device helpers.
 //
-// The work of a call is a list of units, the 64-position chunks of every segment, a segment being
+// The work of a call is a list of units, the chunks of 64 or 128 positions of every segment, a segment being
 // (sequence, key/value head, tile of query rows).  The query rows of a key/value head are its
 // heads / kv_heads query heads of every token, row r = token r / G, head r % G.  How long the
 // sequences are is known on the device only, so every thread block adds the units up itself and
 // takes an equal share of the list: [W c / n, W (c + 1) / n) for block c of n, whatever the lengths
-// are (with fewer units than blocks the first blocks get one each).  A share covers segments whole, or pieces of at most two (its first and its last one); the
-// pieces of a segment leave their running maximum, sum and unnormalised output in the workspace,
-// and k_attention_join adds them up in the order of the list, so results do not depend on timing.
+// are (with fewer units than blocks the first blocks get one each).  A share covers segments whole, or
+// pieces of at most two (its first and its last one); the pieces of a segment leave their running
+// maximum, sum and unnormalised output in the workspace, and k_attention_join adds them up in the order
+// of the list, so results do not depend on timing.
 #pragma once
 
 #include <math.h>
@@ -81,7 +82,7 @@ struct Share {
 
 // All THREADS threads; scratch: THREADS / 32 values.  A group of threads (32, fewer for many sequences,
 // then one for a run of them) adds up the tiles of a sequence; the warp in whose run the share's first
-// unit is looks the tile up, 32 at a time.  (One thread for a sequence took 10 us for 64 tiles.)
+// unit is looks the tile up, 32 at a time.
 template <int THREADS>
 __device__ __forceinline__ void find_share(const AttnArgs& a, const Cut& c, int cta, int ctas,
                                            int64_t* scratch, Share* out) {
@@ -345,8 +346,8 @@ __device__ __forceinline__ int log_runs(int pieces) {
 // Joins the pieces of the segments that are split: that of record c is in blocks c .. last, one piece
 // each.  The work is a list of steps of kJoinThreads threads, over all records; every block adds their
 // numbers up and takes every gridDim.x-th.  A thread holds four outputs of a row and a run of pieces;
-// the runs are added up in order.  (With a block for each record and quarter of the head dimension, 2
-// segments of 60 pieces took 70 us.)
+// the runs are added up in order.  (With a block for each record and quarter of the head dimension, 101
+// rows of one head over two sequences of up to 7681 positions took 82 us instead of 20.)
 template <int D, int R, int MAX_CTAS>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const __grid_constant__ AttnArgs a,
                                                                  int ctas, float gv) {
@@ -357,9 +358,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const __grid_co
   __shared__ float4 s_o[kJoinThreads];
   __shared__ float s_m[kJoinThreads], s_l[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // (The next kernel is not launched early: blocks of the stream kernel that come while this one's leave
-  // spread unevenly over the SMs, and 59 us became of 43 for calls in a row, 16 sequences of up to 4000
-  // positions, head_dim 64.)
+  // (The next kernel is not launched early.  Blocks of a next call's stream kernel that come while this
+  // kernel's blocks leave spread unevenly over the SMs: calls in a row, 16 sequences of up to 4000
+  // positions, head_dim 64, took 59 us each instead of 43.)
   griddep_wait();
   Record recs[kPer];
   int steps[kPer], sum = 0;

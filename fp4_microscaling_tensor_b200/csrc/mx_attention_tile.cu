@@ -12,7 +12,8 @@
 //     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
 //     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
 //   * 1 warp: brings codes and scales into a ring in shared memory (16-byte asynchronous copies; bulk
-//     copies of the 64- to 1024-byte runs that a page holds took 1.4 times as long in all);
+//     copies of the 64- to 1024-byte runs that a page holds took 1.4 times as long without the other
+//     warps' work);
 //   * 2 warps: a chunk's keys, one position per thread, into the K-major B operand of q K^T;
 //   * 4 warps: its values (two of them every other half), 8 positions x D / 8 values per thread,
 //     transposed into the K-major (along the positions) B operand of p V: two positions' codes are
@@ -23,8 +24,14 @@
 //     chunk at a time.
 // Keys, values and codes move in halves of a chunk.  Tensor memory per tile: 128 columns of scores
 // (weights overlay them), D columns of outputs.  (Two buffers of 64 columns would let a tile's scores run
-// ahead of its weights, but products 64 columns wide take as long as those 128 wide: measured 1164 us
-// for 2048 prompt tokens over 16384 positions, 64 heads on 8, against 1067 us.)
+// ahead of its weights, but products 64 columns wide take as long as those 128 wide: for the case below
+// 1164 us when 128 columns took 1067.)
+//
+// What bounds it: 2048 prompt tokens over 16384 positions, 64 heads on 8 of 128, take 960 us, 1.07
+// PFLOP/s or 0.64 of the measured bf16 peak; the tensor pipes, the exponentials' unit and
+// the issue slots are busy half of it each.  Many rows over short sequences are bound by what
+// a piece costs besides its chunks (queries in, outputs out, the first scores and the last outputs alone):
+// 383 tokens of 4 sequences of up to 498 positions, 128 heads on 8, take 109 us; their bytes, 16.
 //
 // Every wait is bounded (mbar_wait below): a block that gives up says so in a device counter
 // (mx_matmul_gave_up), lets its issued products finish, frees its tensor memory and returns; blocks do

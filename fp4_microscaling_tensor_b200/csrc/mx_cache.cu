@@ -14,7 +14,9 @@
 // 16-byte accesses outside for bf16, 8 bytes of codes), of the keys and of the values, so both
 // streams are in flight at once.  Items run along the head, then along the tokens, then across the
 // heads: consecutive lanes touch whole 256-byte rows outside (bf16, head_dim 128) and adjacent
-// slots of one head -- contiguous memory -- in the cache.
+// slots of one head -- contiguous memory -- in the cache.  Measured, 8 heads of 128, bf16: 8192 tokens of
+// 4 sequences in 55 us, 0.72 of the measured copy peak (the rounding's instructions); 16000 of 8 out in
+// 111 us, 0.77.
 #include <string.h>
 
 #include <type_traits>
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(const __grid_constant
     const int64_t slot = in ? a.table.slot(c, b, first + t0 + it.t) : -1;
     const bool ok = slot >= 0;
     const int64_t row = slot + ((int64_t)it.h << c.page_shift);
-    if (!__any_sync(0xffffffffu, ok)) continue;  // idle warps divide nothing (fp32: 10 us, else 14)
+    if (!__any_sync(0xffffffffu, ok)) continue;  // (fp32 divisions of zeros are slow)
     T x[2][4 * kW];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -242,10 +244,10 @@ int tile_items(const CacheArgs& c, int tile_shift) {
   return c.kv_heads * (c.head_dim / 16) << tile_shift;
 }
 
-// Tokens per CTA: 16 (4 and 32 cost a large call up to 9% more, 8192 tokens of 4 sequences), halved
-// while there would be less than four CTAs per SM and two warps keep their items: a small call is one
-// thread's chain of loads, so it goes wide (100 tokens of 4 heads of 256 values read to fp32: 2.2 us;
-// 3.0 if no CTA may have less than 256 items, 4.2 with 512).
+// Tokens per CTA: 16 (8 sequences of 16000 tokens of 8 heads of 128 read to bf16: 109 us, with 4 and 32
+// 112), halved while there would be less than four CTAs per SM and two warps keep their items: a small
+// call is one thread's chain of loads, so it goes wide (100 tokens of 4 heads of 256 values read to fp32:
+// 2.2 us; 3.0 if no CTA may have less than 256 items, 4.2 with 512).
 MoveArgs move_args(const CacheArgs& c, const PageTable& table, const Rows& k, const Rows& v,
                    int64_t batch, int64_t tokens, const int32_t* start, const int32_t* count) {
   MoveArgs a{c, table, {k, v}, tokens, start, count, 4, 0};

@@ -26,6 +26,10 @@
 //     scale makes what the codes say harmless).
 // The warps of a block share its piece's positions evenly and join their results in shared memory at
 // the piece's end.
+//
+// Measured: one token for each of 64 sequences of 819 to 8191 positions, 64 heads on 8 of 128, 77 us, 0.68
+// of the measured copy peak; what bounds it then is the conversion of codes (58 % of the issue slots, ALU
+// and FMA pipes at 52 and 33 %; fixed latencies are the largest stall).
 #include <math.h>
 
 #include "mx_attention.cuh"
