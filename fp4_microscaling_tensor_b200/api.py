@@ -661,6 +661,9 @@ def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, 
     if workspace is None:
         with nullcontext() if stream is None else _allocating(stream):
             workspace = attention_workspace(cache, batch, tokens, heads)
+    elif workspace.dtype != torch.uint8 or workspace.device != cache.device or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous uint8 on the cache's device")
     _call(lib.mx_cache_attention, "mx_cache_attention", cache.device, stream, cache._desc,
           q.data_ptr(), q_strides, batch, tokens, heads, *at, None if tree is None else tree.data_ptr(),
           float(dim ** -0.5 if scale is None else scale), out.data_ptr(), out_strides,
