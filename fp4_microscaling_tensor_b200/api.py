@@ -516,34 +516,47 @@ class KVCache:
 _CACHE_TYPES, _QUERY_TYPES = (torch.bfloat16, torch.float32), (torch.bfloat16,)
 
 
+_stride_arrays = {}  # the library's form of strides, by their values (a decoder's are always the same)
+
+
 def _outside(t, what, cache, dtypes, shape=None, written=False):
     """Checks a [batch, tokens, heads, head_dim] tensor given to a cache call; its strides."""
-    if t.dim() != 4 or t.device != cache.device or t.dtype not in dtypes:
+    own = t.shape
+    if len(own) != 4 or t.device != cache.device or t.dtype not in dtypes:
         raise ValueError(f"{what}: a 4-D tensor [batch, tokens, heads, head_dim] on the cache's "
                          f"device, {' or '.join(str(d).split('.')[1] for d in dtypes)}")
-    if t.shape[3] != cache.head_dim or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)} does not fit")
+    if own[3] != cache.head_dim or (shape is not None and own != shape):
+        raise ValueError(f"{what}: shape {tuple(own)} does not fit")
     strides = t.stride()
     if strides[3] != 1 or (written and 0 in strides and
-                           any(n > 1 and st == 0 for n, st in zip(t.shape, strides))):
+                           any(n > 1 and st == 0 for n, st in zip(own, strides))):
         raise ValueError(f"{what}: the last dimension contiguous"
                          + (", no dimension expanded" if written else ""))
-    return Strides(*strides)
+    array = _stride_arrays.get(strides)
+    if array is None:
+        array = Strides(*strides)
+        if len(_stride_arrays) < 4096:
+            _stride_arrays[strides] = array
+    return array
+
+
+def _numbers(t, name, cache, batch):
+    """Checks a per-sequence number; its address."""
+    if t.dtype != torch.int32 or t.device != cache.device or len(t.shape) != 1 or \
+            t.shape[0] != batch or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 [batch] on the cache's device")
+    return t.data_ptr()
 
 
 def _sequences(cache, batch, table, first, count, what):
     """Checks the page table and the per-sequence numbers; their addresses and the table's shape."""
-    if table.dtype != torch.int32 or table.dim() != 2 or table.device != cache.device or \
-            table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+    shape = table.shape
+    if table.dtype != torch.int32 or len(shape) != 2 or table.device != cache.device or \
+            shape[0] != batch or (shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table: int32 [batch, max_pages] on the cache's device, rows contiguous")
-    for t, name in ((first, what), (count, "count")):
-        if t is None and name == "count":
-            continue
-        if t.dtype != torch.int32 or t.shape != (batch,) or t.device != cache.device or \
-                not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous int32 [batch] on the cache's device")
-    return (table.data_ptr(), table.stride(0) if batch > 1 else 0, table.shape[1],
-            first.data_ptr(), None if count is None else count.data_ptr())
+    return (table.data_ptr(), table.stride(0) if batch > 1 else 0, shape[1],
+            _numbers(first, what, cache, batch),
+            None if count is None else _numbers(count, "count", cache, batch))
 
 
 def _allocating(stream):
@@ -589,9 +602,9 @@ def cache_append(cache, k, v, table, start, count=None, stream=None):
     Tokens behind count (padding) are not read; positions without a page are not written."""
     k_strides = _outside(k, "k", cache, _CACHE_TYPES)
     v_strides = _outside(v, "v", cache, (k.dtype,), k.shape)
-    if k.shape[2] != cache.kv_heads:
+    batch, tokens, kv_heads, _ = k.shape
+    if kv_heads != cache.kv_heads:
         raise ValueError(f"k: {cache.kv_heads} heads in the cache")
-    batch, tokens = k.shape[:2]
     at = _sequences(cache, batch, table, start, count, "start")
     _call(lib.mx_cache_append, "mx_cache_append", cache.device, stream, cache._desc, k.data_ptr(),
           v.data_ptr(), _DT[k.dtype], k_strides, v_strides, batch, tokens, *at)
