@@ -31,7 +31,7 @@
 // PFLOP/s or 0.64 of the measured bf16 peak; the tensor pipes, the exponentials' unit and
 // the issue slots are busy half of it each.  Many rows over short sequences are bound by what
 // a piece costs besides its chunks (queries in, outputs out, the first scores and the last outputs alone):
-// 383 tokens of 4 sequences of up to 498 positions, 128 heads on 8, take 109 us; their bytes, 16.
+// 383 tokens of 4 sequences of up to 498 positions, 128 heads on 8, take 99 us; their bytes, 16.
 //
 // Every wait is bounded (mbar_wait below): a block that gives up says so in a device counter
 // (mx_matmul_gave_up), lets its issued products finish, frees its tensor memory and returns; blocks do
@@ -50,7 +50,6 @@ __device__ unsigned int g_tile_gave_up;
 namespace {
 
 constexpr int kChunk = 128, kHalf = 64;  // positions per chunk, and per step of its loads
-constexpr int kTileStart = 2;  // Cut::start, in chunks
 constexpr int kKeyWarps = 2, kValueWarps = 4;
 constexpr uint32_t kPolls = 1u << 20;
 constexpr float kSlack = 8.0f;
@@ -58,6 +57,10 @@ constexpr float kSlack = 8.0f;
 template <int D, int TILES>
 struct Tile {
   static constexpr int kRows = 128 * TILES;
+  // Cut::start, in chunks (383 tokens of 4 sequences of up to 498 positions, 128 heads on 8 of 128: with 1,
+  // 2, 3, 5 chunks 122, 109, 99, 101 us; a chunk of head_dim 256 takes longer, 914 tokens of 3 sequences,
+  // 64 heads on 8: 304, 298, 315, 321 us)
+  static constexpr int kStart = D == 256 ? 2 : 3;
   static constexpr int kStages = D == 256 ? 2 : 4;       // of half a chunk
   static constexpr int kQ = 128 * D * 2;                // bytes of one tile's queries
   static constexpr int kK = kHalf * D * 2;              // bytes of half a chunk's keys (and values)
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   const uint32_t tmem = tmem_slot;
   griddep_wait();
   griddep_launch_next();
-  const Cut cut{T::kRows, group, kChunk, kTileStart};
+  const Cut cut{T::kRows, group, kChunk, T::kStart};
   find_share<T::kThreads>(a, cut, cta, ctas, s_scan, &s_share);
   // The warp's walk is kept in shared memory (registers are short) and moved on by one lane.
   Walk& walk = s_walk[warp];
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       }
       if (threadIdx.x == 0 && k.c0 == 0 && !whole)
         reinterpret_cast<Record*>(a.workspace)[cta] = {
-            k.b, k.h, k.rt, block_of(walk.u0 + walk.n + kTileStart - 1, s_share),
+            k.b, k.h, k.rt, block_of(walk.u0 + walk.n + T::kStart - 1, s_share),
             min(T::kRows, rows - k.rt * T::kRows)};
       tc_fence_before();
       n += chunks;
