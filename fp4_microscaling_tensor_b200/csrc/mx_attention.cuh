@@ -330,6 +330,12 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, const Seq& s, int t, uin
   return j < 0 || (a.tree ? j < s.count && ((w >> j) & 1) : j <= t);
 }
 
+// Every row from new token t on sees the positions before this one: the old ones and, in a chain, the
+// tokens up to t.  (A tree's words need not name token 0.)
+__device__ __forceinline__ int seen_by_all(const AttnArgs& a, const Seq& s, int t) {
+  return s.base + (a.tree ? 0 : t + 1);
+}
+
 // ---- joining pieces --------------------------------------------------------------------------------
 
 namespace {

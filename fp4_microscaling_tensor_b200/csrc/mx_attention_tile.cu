@@ -371,9 +371,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       if (lane == 0) mbar_arrive(q_full(tile));
 
       const uint64_t word = in && a.tree ? a.tree[k.b * a.tokens + t] : 0;
-      // what every row of the warp sees: up to its first row's token (a tree's rows: the old positions)
-      const int first = a.tree ? 0 : (row - lane) / group;
-      const int plain_end = min(k.end, seq.base + first + 1);
+      const int plain_end = min(k.end, seen_by_all(a, seq, (row - lane) / group));
       const int chunks = k.chunks;
       float m = -INFINITY, mu = 0.0f, lim = -INFINITY;
       float2 l = make_float2(0.0f, 0.0f);

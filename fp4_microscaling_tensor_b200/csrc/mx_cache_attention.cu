@@ -532,7 +532,7 @@ struct Stream {
     seq = Seq(a, b);
     end = p1;
     holes = false;
-    plain_end = min(end, seq.base + (a.tree ? 0 : row0 / group) + 1);
+    plain_end = min(end, seen_by_all(a, seq, row0 / group));
     ahead = p0;
     rows = page_rows(p0);
     rows_next = page_rows(p0 + 512);
