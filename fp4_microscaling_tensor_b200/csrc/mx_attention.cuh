@@ -12,6 +12,7 @@
 // of the list, so results do not depend on timing.
 #pragma once
 
+#include <float.h>
 #include <math.h>
 
 #include "mx_cache.h"
@@ -335,6 +336,33 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, const Seq& s, int t, uin
 __device__ __forceinline__ int seen_by_all(const AttnArgs& a, const Seq& s, int t) {
   return s.base + (a.tree ? 0 : t + 1);
 }
+
+// The softmax's maximum in use and the weights 2^(s mult - mu) of raw scores s.  The maximum moves only
+// when a score exceeds it by kSlack (in log2), so a weight may be up to 2^kSlack.  mu = m mult is rounded;
+// the weights of a row share the factor that this makes, 2^(2^-24 |mu|) at most, and dividing by their sum
+// takes it out again.  But binary16 weights have little room for it, so from |mu| = 2^21 on (`far`) the
+// maximum is taken from the scores before they are multiplied: 2^((s - m) mult).  That happens where the
+// maximum is looked at, so any score of such a row counts as one that may move it.
+constexpr float kSlack = 8.0f, kFar = 0x1p21f;
+struct Maximum {
+  float m, mu, lim;  // raw, what scaled scores are relative to, the score that moves it
+  __device__ __forceinline__ void reset() { m = lim = -INFINITY, mu = 0.0f; }
+  __device__ __forceinline__ bool far(float mult) const {
+    return m > -INFINITY && fabsf(m * mult) >= kFar;
+  }
+  // mn: a raw score, or -infinity if there is none yet.
+  __device__ __forceinline__ void set(float mn, float mult) {
+    m = mn;
+    const bool f = mn == -INFINITY || far(mult);
+    mu = f ? 0.0f : mn * mult;
+    lim = f ? -INFINITY : mn + kSlack / mult;
+  }
+  // What the weights are relative to, in log2, for a join: -infinity if there is no score, finite
+  // otherwise (differences are taken of it).
+  __device__ __forceinline__ float log2(float mult) const {
+    return m == -INFINITY ? m : fminf(fmaxf(m * mult, -FLT_MAX), FLT_MAX);
+  }
+};
 
 // ---- joining pieces --------------------------------------------------------------------------------
 

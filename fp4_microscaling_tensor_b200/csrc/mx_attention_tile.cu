@@ -52,7 +52,6 @@ namespace {
 constexpr int kChunk = 128, kHalf = 64;  // positions per chunk, and per step of its loads
 constexpr int kKeyWarps = 2, kValueWarps = 4;
 constexpr uint32_t kPolls = 1u << 20;
-constexpr float kSlack = 8.0f;
 
 template <int D, int TILES>
 struct Tile {
@@ -373,7 +372,8 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       const uint64_t word = in && a.tree ? a.tree[k.b * a.tokens + t] : 0;
       const int plain_end = min(k.end, seen_by_all(a, seq, (row - lane) / group));
       const int chunks = k.chunks;
-      float m = -INFINITY, mu = 0.0f, lim = -INFINITY;
+      Maximum top;
+      top.reset();
       float2 l = make_float2(0.0f, 0.0f);
       bool ok = true;
       // whether any position of the piece has no page (then its chunks look them up again, below)
@@ -449,29 +449,33 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
                   fmaxf(fmaxf(mx4[e], __uint_as_float(v[i + 2 * e])), __uint_as_float(v[i + 2 * e + 1]));
         }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        const bool grew = mx > lim;
+        const bool grew = mx > top.lim;
         if (__any_sync(0xffffffffu, grew)) {
           float alpha = 1.0f;
           if (grew) {
-            alpha = m == -INFINITY ? 0.0f : ex2((m - mx) * mult);
-            m = mx;
-            mu = m * mult;
-            lim = m + kSlack / mult;
+            const float m = fmaxf(mx, top.m);
+            alpha = top.m == -INFINITY ? 0.0f : ex2((top.m - m) * mult);
+            top.set(m, mult);
             l.x *= alpha;
             l.y *= alpha;
           }
           __syncwarp();
-          if (j > 0) {
-            // (the scores are done, so the products into the outputs issued before them are too)
+          // The outputs so far times alpha (the scores are done, so the products into the outputs issued
+          // before them are too); in front of them, if there are far rows, the scores less the maximum.
+          const bool far = top.far(mult);
+          const float sub = far ? top.m : 0.0f;
+          const bool scores = __any_sync(0xffffffffu, far);
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t x[16];
-              tc_load16(t_o + 16 * c, x);
+          for (int c = scores ? -kChunk / 16 : 0; c < (j > 0 ? D / 16 : 0); ++c) {
+            const uint32_t at = c < 0 ? t_s + kChunk + 16 * c : t_o + 16 * c;
+            const float f = c < 0 ? 1.0f : alpha, less = c < 0 ? sub : 0.0f;
+            uint32_t x[16];
+            tc_load16(at, x);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-              tc_store16(t_o + 16 * c, x);
-            }
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), f, -less));
+            tc_store16(at, x);
           }
+          tc_wait_store();
         }
         __syncwarp();
         // ---- weights: f16 pairs over the scores.  (Rolled up: unrolled, the warps' different code keeps
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                                  make_float2(mult, mult), make_float2(-mu, -mu));
+                                  make_float2(mult, mult), make_float2(-top.mu, -top.mu));
             e = make_float2(ex2(e.x), ex2(e.y));
             l = __fadd2_rn(l, e);
             w[i] = pack_f16x2(e.x, e.y);
@@ -555,9 +559,9 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
         if (whole) {
           if (a.lse)
             a.lse[(k.b * a.tokens + t) * a.heads + head] =
-                sum == 0.0f ? -INFINITY : (mu + log2f(sum)) * 0.6931471805599453f;
+                sum == 0.0f ? -INFINITY : (top.log2(mult) + log2f(sum)) * 0.6931471805599453f;
         } else {
-          part[pr] = m == -INFINITY ? -INFINITY : mu;
+          part[pr] = top.log2(mult);
           part[T::kRows + pr] = sum;
         }
       }

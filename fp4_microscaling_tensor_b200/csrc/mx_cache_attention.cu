@@ -46,9 +46,6 @@ __device__ __forceinline__ int perm(int i) { return i ^ ((i >> 1) & 1); }
 constexpr int kWarps = 4;
 constexpr int kStreamThreads = 32 * kWarps;
 
-constexpr float kSlack = 8.0f;
-
-
 constexpr int kUnit = 64, kStart = 8;  // of the stream kernel's Cut (start: 0 88, 4 83, 8 79, 16 82 us for 64
                                       // sequences of 819 to 8191 positions)
 constexpr int kPart = 32;  // positions computed at a time (more outgrow the instruction cache)
@@ -152,8 +149,8 @@ struct Stream {
   uint32_t q[NT][KS][2];                          // B operand of q K^T (f16 pairs)
   float mult[NT][2];                              // log2 weight per unit of raw score, this lane's
                                                   // two columns (query rows 8 nt + 2 t4, + 1)
-  float m[NT][2], l[NT][2];                       // maximum in use (raw scores), partial sum
-  float mu[NT][2], lim[NT][2];                    // m in log2, and the score that moves it
+  Maximum mx[NT][2];
+  float l[NT][2];                                 // partial sum
   float o[NT][MT][4];
 
   // segment
@@ -263,8 +260,7 @@ struct Stream {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        m[nt][e] = lim[nt][e] = -INFINITY, l[nt][e] = mu[nt][e] = 0.0f;
+      for (int e = 0; e < 2; ++e) mx[nt][e].reset(), l[nt][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -411,33 +407,34 @@ struct Stream {
                 s[nt][mt][2 * half + e] = -INFINITY;
         }
     }
-    // ---- weights, relative to a maximum that follows the scores with a delay: it moves only when a
-    // score exceeds it by kSlack (in log2), so a weight may be up to 2^kSlack, and most tiles need no
+    // ---- weights, relative to a maximum that follows the scores with a delay, so most tiles need no
     // exchange between lanes and leave the outputs as they are
     uint32_t pb[NT][T][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx[2];
+      float top[2];
       bool grew = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(s[nt][0][e], s[nt][0][2 + e]);
+        top[e] = fmaxf(s[nt][0][e], s[nt][0][2 + e]);
 #pragma unroll
-        for (int mt = 1; mt < T; ++mt) mx[e] = fmaxf(mx[e], fmaxf(s[nt][mt][e], s[nt][mt][2 + e]));
-        grew |= mx[e] > lim[nt][e];
+        for (int mt = 1; mt < T; ++mt) top[e] = fmaxf(top[e], fmaxf(s[nt][mt][e], s[nt][mt][2 + e]));
+        grew |= top[e] > mx[nt][e].lim;
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mn = fmaxf(mx[e], m[nt][e]);
+          const float m = mx[nt][e].m;
+          float mn = fmaxf(top[e], m);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
           // (no score yet: nothing to scale)
-          const float alpha = m[nt][e] == -INFINITY ? (mn == -INFINITY ? 1.0f : 0.0f)
-                                                    : ex2((m[nt][e] - mn) * mult[nt][e]);
-          m[nt][e] = mn;
-          mu[nt][e] = mn == -INFINITY ? 0.0f : mn * mult[nt][e];
-          lim[nt][e] = mn == -INFINITY ? mn : mn + kSlack / mult[nt][e];
+          const float alpha = m == -INFINITY ? (mn == -INFINITY ? 1.0f : 0.0f)
+                                             : ex2((m - mn) * mult[nt][e]);
+          mx[nt][e].set(mn, mult[nt][e]);
+          const float sub = mx[nt][e].far(mult[nt][e]) ? mn : 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < T; ++mt) s[nt][mt][e] -= sub, s[nt][mt][2 + e] -= sub;
           l[nt][e] *= alpha;
 #pragma unroll
           for (int i = 0; i < MT; ++i) o[nt][i][e] *= alpha, o[nt][i][2 + e] *= alpha;
@@ -448,7 +445,7 @@ struct Stream {
         float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          w[e] = ex2(fmaf(s[nt][mt][e], mult[nt][e & 1], -mu[nt][e & 1]));
+          w[e] = ex2(fmaf(s[nt][mt][e], mult[nt][e & 1], -mx[nt][e & 1].mu));
           l[nt][e & 1] += w[e];
         }
         // binary16 weights: 2^-11 each, and 2^-25 below the normal range
@@ -615,7 +612,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
           for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
           if (w.g == 0) {
             const int r = 8 * nt + 2 * w.t4 + e;
-            s_m[warp][r] = w.m[nt][e] * w.mult[nt][e];  // (-inf stays)
+            s_m[warp][r] = w.mx[nt][e].log2(w.mult[nt][e]);
             s_l[warp][r] = l;
           }
         }

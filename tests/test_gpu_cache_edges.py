@@ -1,12 +1,13 @@
 """cache_attention at the borders of what its kernels skip or round: trees whose tokens do not see the
-first drafted one, at every place of that one in a masked run (bounds: cache_helpers.attend)."""
+first drafted one, at every place of that one in a masked run; scores of any size float32 holds
+(bounds: cache_helpers.attend)."""
 import numpy as np
 import pytest
 import torch
 
 import fp4_microscaling_tensor_b200 as mx
-from cache_helpers import (G_ONE, check_attention, fill, normal_bf16, pages_for, poisoned,
-                           random_tree)
+from cache_helpers import (G_ONE, assert_close, chain_mask, check_attention, fill, i32,
+                           normal_bf16, pages_for, place, poisoned, random_tree)
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,105 @@ def test_forests_of_equal_sequences(cuda_device):
     tree = np.tile(np.uint64(1) << np.arange(4, dtype=np.uint64), (64, 1))
     q = normal_bf16((64, 4, 8, 64), 2, cuda_device)
     check_attention(cache, table, lengths, None, kv, q, tree=tree)
+
+
+EXPONENTS = (10, 17, 20, 23, 26, 29, 40, 90, 115)  # of the queries' size
+
+
+@pytest.mark.parametrize("tokens", (2, 40))
+@pytest.mark.parametrize("head_dim", (64, 128, 256))
+def test_one_score_far_above_the_rest(cuda_device, head_dim, tokens):
+    """Huge queries: the largest score leads by more than its own float32 error, so a row is that
+    position's values, and lse its score."""
+    rng = np.random.default_rng(head_dim)
+    lengths = [300, 2900]
+    cache, table, kv = setup(lengths, 1, head_dim, 64, rng, cuda_device)
+    ids, ln = i32(table, cuda_device), i32(lengths, cuda_device)
+    checked = 0
+    for e in EXPONENTS:
+        q = normal_bf16((2, tokens, 4, head_dim), e, cuda_device) * 2.0 ** e
+        out, lse = mx.cache_attention(cache, q, ids, ln, lse=True)
+        qn, on, ln_ = (x.float().cpu().numpy().astype(np.float64) for x in (q, out, lse))
+        assert np.isfinite(on).all() and np.isfinite(ln_).all(), e
+        for b, n in enumerate(lengths):
+            k, v = (x[:, 0] for x in kv[b])
+            for h in range(4):
+                s = qn[b, :, h] @ k.T * head_dim ** -0.5
+                off = (head_dim * 2.0 ** -23 * head_dim ** -0.5 * (np.abs(qn[b, :, h]) @ np.abs(k).T)
+                       + np.abs(s) * 2.0 ** -22).max(-1)
+                s = np.where(chain_mask(n, tokens), s, -np.inf)
+                top = s.argmax(-1)
+                order = np.sort(s, -1)
+                # 30: what the others add is below n 2^-40
+                clear = order[:, -1] - order[:, -2] > 2 * off + 30
+                checked += clear.sum()
+                want = v[top[clear]]
+                # the one weight in 11 bits, and bf16
+                assert_close(on[b, clear, h], want, (2.0 ** -8 + 2.0 ** -10) * np.abs(want) + 1e-9,
+                             f"2^{e}, sequence {b}")
+                assert_close(ln_[b, clear, h], order[clear, -1],
+                             off[clear] + np.abs(order[clear, -1]) * 2.0 ** -22, f"2^{e} lse")
+    assert checked > 0.9 * 8 * tokens * (len(EXPONENTS) - 1)  # (at 2^10 some rows are closer)
+
+
+@pytest.mark.parametrize("tokens", (1, 40))
+@pytest.mark.parametrize("fmt", (mx.E4M3, mx.UE5M3))
+@pytest.mark.parametrize("head_dim", (64, 128, 256))
+def test_equal_scores_of_any_size(cuda_device, head_dim, fmt, tokens):
+    """Every position has the same key, so every row is a mean of values whatever the score's size and
+    sign: what rounds the score must not reach the weights."""
+    rng = np.random.default_rng(head_dim)
+    lengths = [40, 2000]
+    table, pages = pages_for(lengths, 32, 1, rng)
+    cache = poisoned(pages, 1, head_dim, 32, 32, fmt, G_ONE, G_ONE, rng, cuda_device)
+    kv = fill(cache, table, lengths, rng)
+    one = 0x38 if fmt == mx.E4M3 else 0x78  # the scale 1
+    code = rng.integers(0, 256, head_dim // 2, dtype=np.uint8) & 0x77  # magnitudes only
+    mags = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
+    key = np.stack((mags[code & 7], mags[code >> 4]), -1).reshape(-1)
+    for b, n in enumerate(lengths):
+        place(cache, table, b, np.arange(n), "k", np.tile(code, (n, 1, 1)),
+              np.full((n, 1, head_dim // 32), one, np.uint8))
+    ids, ln = i32(table, cuda_device), i32(lengths, cuda_device)
+    for e in EXPONENTS:
+        for sign in (1, -1):
+            q = torch.full((2, tokens, 3, head_dim), sign * 1.0078125 * 2.0 ** e,
+                           dtype=torch.bfloat16, device=cuda_device)
+            q[:, :, 1] *= 1.0234375
+            out, lse = mx.cache_attention(cache, q, ids, ln, lse=True, scale=0.1234567)
+            on, ln_ = (x.double().cpu().numpy() for x in (out, lse))
+            for b, n in enumerate(lengths):
+                seen = n - tokens + 1 + np.arange(tokens)
+                v = kv[b][1][:, 0]
+                mean, mag = (np.cumsum(x, 0)[seen - 1] / seen[:, None] for x in (v, np.abs(v)))
+                tol = (2.0 ** -11 + 2 * n * 2.0 ** -23) * mag * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(mean)
+                for h in range(3):
+                    assert_close(on[b, :, h], mean, tol, f"{sign} 2^{e}, sequence {b}")
+                    s = float(q[b, 0, h, 0]) * key.sum() * float(np.float32(0.1234567))
+                    ref = s + np.log(seen)
+                    assert_close(ln_[b, :, h], ref, 2.0 ** -21 + n * 2.0 ** -23 + np.abs(ref) *
+                                 (2.0 ** -22 + head_dim * 2.0 ** -23), f"{sign} 2^{e} lse")
+
+
+@pytest.mark.parametrize("tokens", (1, 40))
+def test_scores_too_small_to_tell_apart(cuda_device, tokens):
+    """A scale so small that all weights are equal, behind positions that have no page: the first
+    positions that a warp sees may give it no score at all."""
+    rng = np.random.default_rng(3)
+    lengths = [700, 90]
+    cache, table, kv = setup(lengths, 1, 64, 16, rng, cuda_device)
+    table[:, :5] = -1
+    q = normal_bf16((2, tokens, 4, 64), 4, cuda_device)
+    out, lse = mx.cache_attention(cache, q, i32(table, cuda_device), i32(lengths, cuda_device),
+                                  lse=True, scale=1e-38)
+    for b, n in enumerate(lengths):
+        for t in range(tokens):
+            v = kv[b][1][80:n - tokens + t + 1, 0]
+            if not len(v):
+                assert not out[b, t].any() and torch.isneginf(lse[b, t]).all()
+                continue
+            mean, mag = v.mean(0), np.abs(v).mean(0)
+            tol = (2.0 ** -11 + 2 * n * 2.0 ** -23) * mag * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(mean)
+            for h in range(4):
+                assert_close(out[b, t, h].double().cpu().numpy(), mean, tol, f"sequence {b}, {t}")
+            assert (lse[b, t] - np.log(len(v))).abs().max() < 2.0 ** -20 + n * 2.0 ** -23
