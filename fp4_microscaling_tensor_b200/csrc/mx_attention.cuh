@@ -338,12 +338,15 @@ __device__ __forceinline__ int seen_by_all(const AttnArgs& a, const Seq& s, int 
 }
 
 // The softmax's maximum in use and the weights 2^(s mult - mu) of raw scores s.  The maximum moves only
-// when a score exceeds it by kSlack (in log2), so a weight may be up to 2^kSlack.  mu = m mult is rounded;
-// the weights of a row share the factor that this makes, 2^(2^-24 |mu|) at most, and dividing by their sum
-// takes it out again.  But binary16 weights have little room for it, so from |mu| = 2^21 on (`far`) the
-// maximum is taken from the scores before they are multiplied: 2^((s - m) mult).  That happens where the
-// maximum is looked at, so any score of such a row counts as one that may move it.
-constexpr float kSlack = 8.0f, kFar = 0x1p21f;
+// when a score exceeds it by kSlack (in log2), and weights are kLift above what that makes them: binary16
+// holds up to 2^16, and the step of the small ones, 2^-24, is 2^-31 of the weight at the maximum then.
+// mu = m mult - kLift is rounded; the weights of a row share the factor that this makes, 2^(2^-24 |mu|) at
+// most, and dividing by their sum takes it out again.  But binary16 has little room for it, so from
+// |m mult| = 2^21 on (`far`) the maximum is taken from the scores before they are multiplied:
+// 2^((s - m) mult + kLift).  That happens where the maximum is looked at, so any score of such a row counts
+// as one that may move it.
+constexpr float kSlack = 8.0f, kLift = 7.0f, kFar = 0x1p21f;
+static_assert(kLift == 7.0f, "log_sum takes 2^7 out of the weights' sum");
 struct Maximum {
   float m, mu, lim;  // raw, what scaled scores are relative to, the score that moves it
   __device__ __forceinline__ void reset() { m = lim = -INFINITY, mu = 0.0f; }
@@ -354,15 +357,21 @@ struct Maximum {
   __device__ __forceinline__ void set(float mn, float mult) {
     m = mn;
     const bool f = mn == -INFINITY || far(mult);
-    mu = f ? 0.0f : mn * mult;
+    mu = f ? -kLift : fmaf(mn, mult, -kLift);
     lim = f ? -INFINITY : mn + kSlack / mult;
   }
   // What the weights are relative to, in log2, for a join: -infinity if there is no score, finite
   // otherwise (differences are taken of it).
   __device__ __forceinline__ float log2(float mult) const {
-    return m == -INFINITY ? m : fminf(fmaxf(m * mult, -FLT_MAX), FLT_MAX);
+    return m == -INFINITY ? m : fminf(fmaxf(fmaf(m, mult, -kLift), -FLT_MAX), FLT_MAX);
   }
 };
+
+// The natural logarithm of the sum of the exponentials, from the sum l of weights relative to mu.
+__device__ __forceinline__ float log_sum(float mu, float l) {
+  return l == 0.0f ? -INFINITY
+                   : ((mu + kLift) + log2f(l * 0x1p-7f)) * 0.6931471805599453f;
+}
 
 // ---- joining pieces --------------------------------------------------------------------------------
 
@@ -492,9 +501,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const __grid_co
                                 d) =
           make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
       if (a.lse && d == 0)
-        a.lse[(rec.b * a.tokens + t) * a.heads + head] =
-            l == 0.0f ? -INFINITY
-                      : ((mx == -INFINITY ? 0.0f : mx) + log2f(l)) * 0.6931471805599453f;
+        a.lse[(rec.b * a.tokens + t) * a.heads + head] = log_sum(mx, l);
     }
     __syncthreads();
   }

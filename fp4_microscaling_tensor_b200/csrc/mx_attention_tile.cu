@@ -9,8 +9,8 @@
 // One thread block per SM, whose warps have one job each:
 //   * 4 warps per 128-row tile: load and scale the queries (f16, 128-byte-swizzled shared memory);
 //     then per chunk, one row per thread: read the scores from tensor memory, mask, weights
-//     p = 2^(s c - m c), running sum, write p as f16 over the scores; scale the outputs when the
-//     maximum moves (by more than 2^8: weights may be up to 2^8); at the end read the outputs;
+//     p = 2^(s c - m c + 7), running sum, write p as f16 over the scores; scale the outputs when the
+//     maximum moves (by more than 2^8: weights may be up to 2^15); at the end read the outputs;
 //   * 1 warp: brings codes and scales into a ring in shared memory (16-byte asynchronous copies; bulk
 //     copies of the 64- to 1024-byte runs that a page holds took 1.4 times as long without the other
 //     warps' work);
@@ -557,9 +557,7 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
       }
       if (in) {
         if (whole) {
-          if (a.lse)
-            a.lse[(k.b * a.tokens + t) * a.heads + head] =
-                sum == 0.0f ? -INFINITY : (top.log2(mult) + log2f(sum)) * 0.6931471805599453f;
+          if (a.lse) a.lse[(k.b * a.tokens + t) * a.heads + head] = log_sum(top.log2(mult), sum);
         } else {
           part[pr] = top.log2(mult);
           part[T::kRows + pr] = sum;

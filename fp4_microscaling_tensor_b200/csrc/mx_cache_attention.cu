@@ -448,7 +448,7 @@ struct Stream {
           w[e] = ex2(fmaf(s[nt][mt][e], mult[nt][e & 1], -mx[nt][e & 1].mu));
           l[nt][e & 1] += w[e];
         }
-        // binary16 weights: 2^-11 each, and 2^-25 below the normal range
+        // binary16 weights: 2^-11 each, and 2^-32 of the maximum's below the normal range
         pb[nt][mt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
         pb[nt][mt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
       }
@@ -666,8 +666,7 @@ __global__ void __launch_bounds__(kStreamThreads, Geometry<D, NT>::kBlocks)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out.p) + row_offset(a.out, b, t, head) +
                                     d) = v;
           if (a.lse && d == 0)
-            a.lse[(b * a.tokens + t) * a.heads + head] =
-                l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+            a.lse[(b * a.tokens + t) * a.heads + head] = log_sum(mu, l);
         } else {
           float4* dst = reinterpret_cast<float4*>(part + 2 * R + r * D + d);
           dst[0] = make_float4(y[0], y[1], y[2], y[3]);

@@ -405,8 +405,8 @@ MX_API size_t mx_cache_attention_workspace_size(int64_t batch, int64_t tokens, i
  *   workspace  device scratch of at least mx_cache_attention_workspace_size() bytes; needs no
  *          initialisation.  Calls that may run at the same time need one each.
  * Scores, softmax statistics and sums are kept in float32; the softmax weights enter the product
- * with V as binary16 relative to the row's largest (2^-11 each).  Results do not depend on the order
- * in which thread blocks run. */
+ * with V as binary16 (each rounded by 2^-11 of itself, and by 2^-32 of the row's largest where that is
+ * more).  Results do not depend on the order in which thread blocks run. */
 MX_API mx_status mx_cache_attention(const mx_cache_t* cache, const void* q,
                                     const int64_t* q_strides, int64_t batch, int64_t tokens,
                                     int64_t heads, const int32_t* table, int64_t table_stride,

@@ -1,6 +1,6 @@
 """cache_attention at the borders of what its kernels skip or round: trees whose tokens do not see the
-first drafted one, at every place of that one in a masked run; scores of any size float32 holds
-(bounds: cache_helpers.attend)."""
+first drafted one, at every place of that one in a masked run; scores of any size float32 holds; many
+small weights beside a few large ones (bounds: cache_helpers.attend)."""
 import numpy as np
 import pytest
 import torch
@@ -158,3 +158,44 @@ def test_scores_too_small_to_tell_apart(cuda_device, tokens):
             for h in range(4):
                 assert_close(out[b, t, h].double().cpu().numpy(), mean, tol, f"sequence {b}, {t}")
             assert (lse[b, t] - np.log(len(v))).abs().max() < 2.0 ** -20 + n * 2.0 ** -23
+
+
+@pytest.mark.parametrize("batch,tokens", ((444, 1), (100, 1), (148, 40), (30, 300)))
+@pytest.mark.parametrize("head_dim,fmt", ((64, mx.E4M3), (128, mx.UE5M3), (256, mx.E4M3)))
+def test_many_small_weights_beside_a_few_large_ones(cuda_device, head_dim, fmt, batch, tokens):
+    """A position in 8192 has a score x above the rest (in log2) and a value of 0, the rest have 1:
+    what the rest add up to must not be lost.  (All sequences share their pages; x reaches to where a
+    weight is 2^-29 of the largest.)
+
+    Bound: a weight, relative to the largest, is rounded by 2^-11 of itself and 2^-32; the rest as in
+    cache_helpers.attend, with scores that are exact but for their scaling (2^-22 x) and the
+    exponential (2^-21)."""
+    n, page = 131072 if batch == 444 else 65536, 256
+    one = 0x38 if fmt == mx.E4M3 else 0x78  # the scale 1
+    shape = (n // page, 1, page, head_dim // 2)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=cuda_device) for _ in range(2))
+    sink = torch.arange(n, device=cuda_device) % 8192 == 5
+    k.view(n, -1)[sink] = 0x22    # 1, 1
+    v.view(n, -1)[~sink] = 0x22
+    scales = torch.full((n // page, 1, page, head_dim // 32), one, dtype=torch.uint8,
+                        device=cuda_device)
+    cache = mx.KVCache.from_buffers(k, scales, v, scales, fmt=fmt)
+    table = torch.arange(n // page, dtype=torch.int32, device=cuda_device).expand(batch, -1)
+    q = torch.ones(batch, tokens, 1, head_dim, dtype=torch.bfloat16, device=cuda_device)
+    seen = n - tokens + 1 + np.arange(tokens)
+    sinks = (seen - 6) // 8192 + 1
+    for x in (20.0, 24.9, 25.1, 27.0, 29.0):
+        scale = float(np.float32(x * np.log(2) / head_dim))
+        out, lse = mx.cache_attention(cache, q, table, i32([n] * batch, cuda_device), lse=True,
+                                      scale=scale)
+        w = np.exp(-scale * head_dim)
+        total = sinks + (seen - sinks) * w
+        want = (seen - sinks) * w / total
+        e = 2.0 ** -22 * x + 2.0 ** -21
+        tol = (2 * e + 2.0 ** -11 + 2 * n * 2.0 ** -23) * want + n * 2.0 ** -32 / total
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * want
+        on, ln = (t.double().cpu().numpy()[:, :, 0] for t in (out, lse))
+        for b in range(batch):
+            assert_close(on[b], np.tile(want[:, None], head_dim), tol[:, None], f"2^-{x}, {b}")
+            assert_close(ln[b], scale * head_dim + np.log(total), e + n * 2.0 ** -23 + 2.0 ** -17,
+                         f"2^-{x}, {b} lse")
