@@ -391,7 +391,8 @@ mx_status mx_matmul_prepare_scales(const uint8_t* scales, int64_t rows, int64_t 
 mx_status mx_matmul_gave_up(unsigned int* count) {
   if (!count) return MX_ERR_INVALID_ARG;
   unsigned int attention = 0;
-  cudaError_t e = mxk::matmul_gave_up(count);
+  cudaError_t e = cudaDeviceSynchronize();  // also the streams that the default one does not wait for
+  if (e == cudaSuccess) e = mxk::matmul_gave_up(count);
   if (e == cudaSuccess) e = mxk::attention_gave_up(&attention);
   if (e == cudaSuccess) *count += attention;
   return from_cuda(e);

@@ -904,10 +904,8 @@ cudaError_t run_tile(const AttnArgs& a, cudaStream_t stream, int* launches) {
 }  // namespace attn
 
 cudaError_t attention_gave_up(unsigned int* count) {
-  const unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(count, attn::g_tile_gave_up, sizeof(unsigned int));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(attn::g_tile_gave_up, &zero, sizeof(unsigned int));
-  return e;
+  static std::atomic<unsigned int> seen[kMaxDevices];
+  return counted_since(attn::g_tile_gave_up, seen, count);
 }
 
 }  // namespace mxk

@@ -73,7 +73,7 @@ struct AttnArgs {
 size_t attention_workspace_bytes(int64_t batch, int64_t tokens, int heads, int kv_heads,
                                  int head_dim);
 cudaError_t run_cache_attention(const AttnArgs& a, cudaStream_t stream, int* launches);
-// Reads and clears the count of attention thread blocks whose bounded waits ran out (synchronizes).
+// The count of attention thread blocks whose bounded waits have run out since the last call.
 cudaError_t attention_gave_up(unsigned int* count);
 
 }  // namespace mxk

@@ -58,6 +58,19 @@ inline cudaError_t allow_dynamic_smem(std::atomic<bool>* flags, K* kern, int byt
   return e;
 }
 
+// What a device counter that only grows has gained on the current device since the last call with these
+// `seen` (one array per counter), which is not reset, so that no count falls between a read and a reset.
+inline cudaError_t counted_since(const unsigned int& symbol, std::atomic<unsigned int>* seen,
+                                 unsigned int* count) {
+  int dev = 0;
+  unsigned int now = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&now, symbol, sizeof(now));
+  if (e == cudaSuccess) *count = now - seen[dev].exchange(now);
+  return e;
+}
+
 // Persistent grid for a grid-stride kernel with kThreads threads: enough CTAs to fill every SM
 // at the kernel's occupancy, never more than the work needs (items / (threads * items_per_iter)).
 inline int persistent_grid(const void* kern, int64_t nitems, int items_per_iter,
@@ -258,7 +271,7 @@ cudaError_t run_dequant_matmul(const void* a, int64_t m, int64_t k, const uint8_
 int64_t mma_scales_bytes(int64_t rows, int64_t k);
 cudaError_t run_scales_to_mma(const uint8_t* scales, int64_t rows, int64_t k, uint8_t* out,
                               cudaStream_t stream, int* launches);
-// Reads and clears the count of matmul CTAs whose bounded waits ran out (synchronizes).
+// The count of matmul CTAs whose bounded waits have run out since the last call.
 cudaError_t matmul_gave_up(unsigned int* count);
 // Test hook: marks the most recent matmul launch as abandoned on the current device, as a CTA
 // whose waits ran out does (synchronizes).

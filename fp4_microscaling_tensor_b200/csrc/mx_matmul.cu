@@ -1115,10 +1115,8 @@ cudaError_t run_scales_to_mma(const uint8_t* scales, int64_t rows, int64_t k, ui
 }
 
 cudaError_t matmul_gave_up(unsigned int* count) {
-  const unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(count, g_mm_gave_up, sizeof(unsigned int));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_mm_gave_up, &zero, sizeof(unsigned int));
-  return e;
+  static std::atomic<unsigned int> seen[kMaxDevices];
+  return counted_since(g_mm_gave_up, seen, count);
 }
 
 cudaError_t matmul_abandon_last() {

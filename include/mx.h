@@ -19,9 +19,10 @@
  *     allocates and never synchronizes (except the calls documented as synchronizing).  State that
  *     outlives a call: the diagnostic launch counter (mx_kernel_launches), the scratch array of
  *     mx_error_stats_noalloc (shared by its calls on a device, see there), the test hook's armed
- *     failures (mx_test_fail_next_calls), and for mx_matmul a per-device count of thread blocks
- *     whose bounded waits ran out plus the generation number of the last launch that gave up
- *     (see mx_matmul_gave_up; later launches are not affected by it).
+ *     failures (mx_test_fail_next_calls), for mx_matmul, mx_dequant_matmul and mx_cache_attention a
+ *     per-device count of thread blocks whose bounded waits ran out (see mx_matmul_gave_up), and for
+ *     the first two the generation number of the last launch that gave up (later launches are not
+ *     affected by it).
  *   - Everything is enqueued on `stream` (0 = the legacy default stream); results are valid after
  *     the caller synchronizes that stream.
  *   - Arguments are checked on the host before anything is enqueued; a non-OK status means nothing
@@ -311,8 +312,8 @@ MX_API mx_status mx_dequant_matmul(const void* a, int64_t m, int64_t k, const ui
                                    cudaStream_t stream);
 
 /* Number of thread blocks of mx_matmul, mx_dequant_matmul and mx_cache_attention that stopped waiting
- * since the previous call (0 in normal operation), written to *count (host memory); clears the
- * count.  Synchronizes the device. */
+ * since the previous call (0 in normal operation), written to *count (host memory); the next call
+ * counts from here.  Synchronizes the device, every stream of it. */
 MX_API mx_status mx_matmul_gave_up(unsigned int* count);
 
 /* Test hook (no counterpart in the pages): marks the most recent mx_matmul / mx_matmul_pair launch
@@ -406,7 +407,9 @@ MX_API size_t mx_cache_attention_workspace_size(int64_t batch, int64_t tokens, i
  *          initialisation.  Calls that may run at the same time need one each.
  * Scores, softmax statistics and sums are kept in float32; the softmax weights enter the product
  * with V as binary16 (each rounded by 2^-11 of itself, and by 2^-32 of the row's largest where that is
- * more).  Results do not depend on the order in which thread blocks run. */
+ * more).  Results do not depend on the order in which thread blocks run.  Every wait inside the
+ * kernels is bounded; a call whose waits ran out leaves out and lse unspecified and is counted by
+ * mx_matmul_gave_up. */
 MX_API mx_status mx_cache_attention(const mx_cache_t* cache, const void* q,
                                     const int64_t* q_strides, int64_t batch, int64_t tokens,
                                     int64_t heads, const int32_t* table, int64_t table_stride,

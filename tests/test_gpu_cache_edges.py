@@ -199,3 +199,19 @@ def test_many_small_weights_beside_a_few_large_ones(cuda_device, head_dim, fmt, 
             assert_close(on[b], np.tile(want[:, None], head_dim), tol[:, None], f"2^-{x}, {b}")
             assert_close(ln[b], scale * head_dim + np.log(total), e + n * 2.0 ** -23 + 2.0 ** -17,
                          f"2^-{x}, {b} lse")
+
+
+def test_the_count_of_ended_waits_is_read_behind_every_stream(cuda_device):
+    """matmul_gave_up synchronizes the device: work on a stream that the default one does not wait for
+    is over when it returns, so nothing that the work would add is missed."""
+    a = torch.randn(8192, 8192, device=cuda_device).bfloat16()
+    side, over = torch.cuda.Stream(), torch.cuda.Event()
+    assert mx.matmul_gave_up() == 0  # (a first call loads the kernels, which waits by itself)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(60):  # about 40 ms
+            b = a @ a
+        over.record()
+    assert mx.matmul_gave_up() == 0
+    assert over.query()
+    del b
