@@ -64,8 +64,9 @@ __device__ __forceinline__ T block_max(T m, int lanes) {
   return m;
 }
 
-// 16 bf16 values (8 words) -> two words of codes and the block's scale code.  Infinities saturate
-// and a block of NaNs takes the largest scale, so that no NaN scale is ever stored.
+// 16 bf16 values (8 words) -> two words of codes and the block's scale code.  Infinities saturate and
+// NaNs do not count for the scale (the maximum drops them beside other values, the comparison where there
+// are none), so that no NaN scale is ever stored; a NaN itself becomes code 6.
 template <int FMT>
 __device__ __forceinline__ uint32_t quantize16(const uint32_t (&w)[8], int lanes, float g, float r6,
                                                uint2& codes) {
@@ -73,7 +74,8 @@ __device__ __forceinline__ uint32_t quantize16(const uint32_t (&w)[8], int lanes
 #pragma unroll
   for (int k = 1; k < 8; ++k) t = bf16x2_absmax(t, w[k]);
   t &= 0x7FFF7FFFu;
-  const uint32_t m = min(block_max(max(t & 0xFFFFu, t >> 16), lanes), 0x7F80u);
+  const uint32_t lo = t & 0xFFFFu, hi = t >> 16;
+  const uint32_t m = block_max(max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi), lanes);
   const uint32_t sc = encode_scale<FMT>(snap21(__fmul_rn(__uint_as_float(m << 16), r6)));
   const float D = divisor<FMT>(sc, g);
   const float r = D > 0.0f ? __frcp_rn(D) : 0.0f;  // zero scale: every code is +-0
@@ -102,7 +104,7 @@ __device__ __forceinline__ uint32_t quantize16(const float (&x)[16], int lanes, 
   const float D = divisor<FMT>(sc, g);
   float q[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) q[k] = D > 0.0f ? __fdiv_rn(x[k], D) : copysignf(0.0f, x[k]);
+  for (int k = 0; k < 16; ++k) q[k] = D > 0.0f ? __fdiv_rn(x[k], D) : x[k] * 0.0f;  // (signed zeros)
   codes.x = cvt_e2m1x8(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
   codes.y = cvt_e2m1x8(q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]);
   return sc;

@@ -365,7 +365,8 @@ typedef struct {
 /* Quantizes keys and values into the cache: token t < count[b] of sequence b becomes position
  * start[b] + t, by the rule of mx_quantize (the same codes and scales, bit for bit).
  *   k, v   [batch, tokens, kv_heads, head_dim] of type xt.  Values should be finite; an infinity
- *          stores the largest magnitude, a NaN a finite one (never a NaN scale).
+ *          stores the largest magnitude, a NaN the largest of its block's scale, for which it does not
+ *          count (never a NaN scale).
  * Sequences of one call must not write the same slot. */
 MX_API mx_status mx_cache_append(const mx_cache_t* cache, const void* k, const void* v, mx_dtype xt,
                                  const int64_t* k_strides, const int64_t* v_strides, int64_t batch,
