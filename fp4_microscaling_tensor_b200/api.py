@@ -559,10 +559,11 @@ def _sequences(cache, batch, table, first, count, what):
             None if count is None else _numbers(count, "count", cache, batch))
 
 
-def _allocating(stream):
-    """Where outputs and scratch are allocated (and zeroed) when the caller names a stream: there."""
+def _allocating(stream, device):
+    """Where outputs and scratch are allocated (and zeroed) when the caller names a stream: there.  (A
+    handle is taken for a stream of this device, not of the current one.)"""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(stream)))
+                             else torch.cuda.ExternalStream(ctypes_stream(stream), device=device))
 
 
 # the current stream's handle without a Stream object around it (a decoder's step makes many small
@@ -590,7 +591,7 @@ def _new(shape, dtype, cache, count, stream):
     make = torch.empty if count is None else torch.zeros
     if stream is None:
         return make(shape, dtype=dtype, device=cache.device)
-    with _allocating(stream):
+    with _allocating(stream, cache.device):
         return make(shape, dtype=dtype, device=cache.device)
 
 
@@ -672,7 +673,7 @@ def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, 
                             or lse.device != cache.device or not lse.is_contiguous()):
         raise ValueError("lse: contiguous float32 [batch, tokens, heads] on the cache's device")
     if workspace is None:
-        with nullcontext() if stream is None else _allocating(stream):
+        with nullcontext() if stream is None else _allocating(stream, cache.device):
             workspace = attention_workspace(cache, batch, tokens, heads)
     elif workspace.dtype != torch.uint8 or workspace.device != cache.device or \
             not workspace.is_contiguous():

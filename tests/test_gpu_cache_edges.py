@@ -215,3 +215,23 @@ def test_the_count_of_ended_waits_is_read_behind_every_stream(cuda_device):
     assert mx.matmul_gave_up() == 0
     assert over.query()
     del b
+
+
+@pytest.mark.parametrize("tokens", (1, 40))
+def test_streams_by_handle(cuda_device, tokens):
+    """A stream's handle, the default stream's (0) too, does what the stream object does."""
+    rng = np.random.default_rng(tokens)
+    lengths = [300, 90]
+    cache, table, kv = setup(lengths, 1, 64, 16, rng, cuda_device)
+    q = normal_bf16((2, tokens, 4, 64), 4, cuda_device)
+    args = (i32(table, cuda_device), i32(lengths, cuda_device))
+    ref = mx.cache_attention(cache, q, *args, lse=True)
+    read = mx.cache_read(cache, args[0], i32([0, 0], cuda_device), args[1], 300)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        got = mx.cache_attention(cache, q, *args, lse=True, stream=stream)
+        back = mx.cache_read(cache, args[0], i32([0, 0], cuda_device), args[1], 300, stream=stream)
+        torch.cuda.synchronize()
+        for a, b in zip((*ref, *read), (*got, *back)):
+            assert torch.equal(a, b)
