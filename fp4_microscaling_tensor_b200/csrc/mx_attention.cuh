@@ -161,7 +161,7 @@ __device__ __forceinline__ int block_of(int64_t u, const Share& sh) {
   return (int)divide((u + 1) * sh.blocks - 1, sh.total);
 }
 
-// A walk over the pieces of a share: segment (b, h, rt), its 64-position chunks c0 .. c1 - 1 of `n`.
+// A walk over the pieces of a share: segment (b, h, rt), its chunks (of Cut::unit positions) c0 .. c1 - 1 of `n`.
 struct Walk {
   int64_t b;
   int h, rt;
@@ -282,18 +282,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
-}
-
-// Eight E2M1 codes -> four f16 pairs, byte by byte.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {

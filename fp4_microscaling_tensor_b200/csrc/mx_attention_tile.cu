@@ -27,8 +27,9 @@
 // ahead of its weights, but products 64 columns wide take as long as those 128 wide: for the case below
 // 1164 us when 128 columns took 1067.)
 //
-// What bounds it: 2048 prompt tokens over 16384 positions, 64 heads on 8 of 128, take 960 us, 1.07
-// PFLOP/s or 0.64 of the measured bf16 peak; the tensor pipes, the exponentials' unit and
+// What bounds it: 2048 prompt tokens over 16384 positions, 64 heads on 8 of 128, take 964 us at 1965 MHz,
+// 1.07 PFLOP/s or 0.64 of the measured bf16 burst peak (1040 us at the 1825 MHz that the power cap leaves
+// of it after a second, 0.69 of the peak measured that way); the tensor pipes, the exponentials' unit and
 // the issue slots are busy half of it each.  Many rows over short sequences are bound by what
 // a piece costs besides its chunks (queries in, outputs out, the first scores and the last outputs alone):
 // 383 tokens of 4 sequences of up to 498 positions, 128 heads on 8, take 99 us; their bytes, 16.
@@ -855,10 +856,8 @@ __global__ void __launch_bounds__(Tile<D, TILES>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
-    bool ok = true;
     int unused = 0;
-    if (lane == 0) ok = mbar_wait(done, 0, &unused);
-    (void)ok;
+    if (lane == 0) mbar_wait(done, 0, &unused);
     __syncwarp();
     if (lane == 0 && *gave_up) atomicAdd(&g_tile_gave_up, 1u);
     tc_fence_after();

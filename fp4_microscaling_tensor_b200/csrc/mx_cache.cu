@@ -14,9 +14,9 @@
 // 16-byte accesses outside for bf16, 8 bytes of codes), of the keys and of the values, so both
 // streams are in flight at once.  Items run along the head, then along the tokens, then across the
 // heads: consecutive lanes touch whole 256-byte rows outside (bf16, head_dim 128) and adjacent
-// slots of one head -- contiguous memory -- in the cache.  Measured, 8 heads of 128, bf16: 8192 tokens of
-// 4 sequences in 55 us, 0.72 of the measured copy peak (the rounding's instructions); 16000 of 8 out in
-// 111 us, 0.77.
+// slots of one head -- contiguous memory -- in the cache.  Measured, 8 heads of 128, blocks of 32, against
+// the bytes at the measured copy peak: 24862 tokens of 4 sequences of up to 8192 in, bf16 26 us (0.77), fp32
+// 56 us (0.64); 106205 of 8 of up to 16000 out, bf16 111 us (0.77), fp32 298 us (0.51).
 #include <string.h>
 
 #include <type_traits>
@@ -203,21 +203,13 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const __grid_constant__
     for (int s = 0; s < 2; ++s) {
       const float D = __fmul_rn(scale_value((int)sc[s], FMT), g[s]);  // exact
       const uint32_t cw[2] = {codes[s].x, codes[s].y};
-      uint32_t h[8];
+      uint32_t h[2][4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-            "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-            : "=r"(h[4 * k]), "=r"(h[4 * k + 1]), "=r"(h[4 * k + 2]), "=r"(h[4 * k + 3])
-            : "r"(cw[k]));
+      for (int k = 0; k < 2; ++k) e2m1x8_to_f16(cw[k], h[k]);
       float y[16];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h[k])),
+        const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h[k >> 2][k & 3])),
                                     make_float2(D, D));  // exact
         y[2 * k] = v.x;
         y[2 * k + 1] = v.y;

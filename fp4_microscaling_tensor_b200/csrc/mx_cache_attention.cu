@@ -6,9 +6,8 @@
 // weights p = 2^((s - m') c), l = l 2^((m - m') c) + sum p, o = o 2^((m - m') c) + p V.
 //
 // k_attention_stream, for few query rows per key/value head (a decoder's steps, chains and small
-// trees of drafted tokens): what bounds it is reading the cache, 1 + 2 / N bytes per position and
-// head dimension, and next to it the instructions that turn codes into f16 (about 2 per pair of
-// codes), so both are what the layout is made for:
+// trees of drafted tokens): it has to read the cache, 1 + 2 / N bytes per position and head dimension,
+// and turn codes into f16 (about 2 instructions per pair of codes); the layout is made for both:
 //   * mma.sync m16n8k16 with the positions (scores) or the head dimension (outputs) as its 16 rows
 //     and the query rows as its 8 columns: 8 query rows -- 8 query heads that share a key/value head
 //     -- fill it.  The 128 lanes-deep tcgen05 tile would be 6 % full; the tensor pipe is not what
@@ -27,9 +26,10 @@
 // The warps of a block share its piece's positions evenly and join their results in shared memory at
 // the piece's end.
 //
-// Measured: one token for each of 64 sequences of 819 to 8191 positions, 64 heads on 8 of 128, 77 us, 0.68
-// of the measured copy peak; what bounds it then is the conversion of codes (58 % of the issue slots, ALU
-// and FMA pipes at 52 and 33 %; fixed latencies are the largest stall).
+// Measured: one token for each of 64 sequences of 819 to 8191 positions, 64 heads on 8 of 128, 78 us at 1965
+// MHz, 0.67 of the measured copy peak (83 us at the 1840 MHz that the power cap leaves of it after a
+// second).  Neither memory nor the issue slots (57 % in use, ALU and FMA pipes 51 and 32 %) bound it then:
+// with 2.8 warps per scheduler the fixed latencies of dependent instructions are the largest stall.
 #include <math.h>
 
 #include "mx_attention.cuh"
@@ -742,7 +742,7 @@ cudaError_t dispatch_rows(const AttnArgs& a, cudaStream_t stream, int* launches)
 
 // Above this many query rows per key/value head the tile kernel takes over, whose time hardly depends on
 // the rows up to 128.  32 rows there and here (16 sequences of up to 8000 positions): head_dim 64 100 and
-// 56 us, 128 117 and 85, 256 302 and 201; of up to 600: 27 and 24, 34 and 26, 53 and 44.  64 rows: 120
+// 56 us, 128 120 and 86, 256 305 and 197; of up to 600: 27 and 24, 34 and 26, 54 and 44.  64 rows: 120
 // there, 250 here (head_dim 128).
 static constexpr int kStreamRows = 32;
 
