@@ -649,7 +649,8 @@ def cache_attention(cache, q, table, length, count=None, tree=None, scale=None, 
     already appended.  A token sees every earlier position and, of this call's tokens, itself and
     those before it, or with tree (int64 [batch, tokens], tokens <= 64) token j where bit j of its
     word is set: the ancestors, and usually itself, in a tree of drafted tokens.  Tokens that see
-    nothing get zeros.  After a draft is verified, append the accepted tokens' keys and values again
+    nothing get zeros.  Every position below length that has a page must have been written, also those that
+    no token of a tree sees.  After a draft is verified, append the accepted tokens' keys and values again
     behind each other.
 
     scale defaults to head_dim ** -0.5.  Returns out (bf16, like q), or (out, lse) when lse is True

@@ -389,7 +389,9 @@ MX_API size_t mx_cache_attention_workspace_size(int64_t batch, int64_t tokens, i
 
 /* Attention of each sequence's newest tokens over its cache, those tokens included:
  *     out[b, t, h] = sum_p softmax_p(scale * q[b, t, h] . K[p, h / (heads / kv_heads)]) V[p, ...]
- * over the positions p that token t sees, K and V the exact dequantized values.  Sequence b is
+ * over the positions p that token t sees, K and V the exact dequantized values.  (Every position
+ * below length[b] that has a page must have been written: an E4M3 NaN scale in one reaches all rows, also
+ * those that do not see it.)  Sequence b is
  * length[b] positions long (cut to what the table reaches); its count[b] newest ones are those of
  * this call's tokens, so token t is position length[b] - count[b] + t and mx_cache_append comes
  * first.  Token t sees every position before the newest ones, and of those
